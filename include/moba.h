@@ -358,6 +358,163 @@ MOBA_API moba_status_t moba_check_index(const moba_shape_t* shape, int32_t exact
                                         int32_t* offsets, const int32_t* rows, int* status,
                                         moba_stream_t stream);
 
+/* ---- norm and position rotation of queries and keys ----------------------- */
+
+/* What precedes the attention in a layer (the pages use a Llama-shaped model,
+ * [summary] section 3, and position interpolation during context extension,
+ * section 5; they print no formula for either).  For one head x of d =
+ * head_dim numbers of the token at position p:
+ *   y = x r w,  r = (mean(x^2) + eps)^(-1/2),  w the head-shared weights [d]
+ *   pair i < rot_dim / 2:  (a, b) -> (a c - b s, b c + a s),
+ *     c, s = cos, sin(p inv_freq[i]);  (a, b) = (y[i], y[i + rot_dim / 2]), or
+ *     (y[2i], y[2i + 1]) with `interleaved`; channels from rot_dim on stay y.
+ * The angle is computed in 64 bits (positions of 10M and more keep their full
+ * accuracy); the frequencies are the caller's, so that scaled or interpolated
+ * positions are scaled frequencies. */
+typedef struct {
+  int32_t rot_dim;      /* rotated channels: a multiple of 16, 0 .. head_dim       */
+  int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)    */
+  int32_t weight_dtype; /* moba_dtype_t of the norm weights and their gradients    */
+  float eps;            /* >= 0                                                    */
+} moba_rope_t;
+
+typedef struct {
+  int32_t tokens;       /* T >= 0: rows of q and k (batch entries one after another) */
+  int32_t hq, hkv;      /* heads; hq % hkv == 0                                    */
+  int32_t head_dim;     /* 64 or 128                                               */
+  int32_t dtype;        /* moba_dtype_t of q, k and the results                    */
+  int64_t q_stride;     /* elements between tokens of the INPUTS q, k (rows of a   */
+  int64_t k_stride;     /* fused projection); 0 = dense.  Multiples of 16 bytes.   */
+  moba_rope_t rope;
+} moba_rope_shape_t;
+
+/* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31). */
+MOBA_API moba_status_t moba_check_rope_shape(const moba_rope_shape_t* shape);
+
+/* Norm and rotation of every query and key head, one kernel.
+ *   q [T, hq, d], k [T, hkv, d]    dtype, token strides as in shape   (read)
+ *   q_weight, k_weight [d]         weight_dtype                       (read)
+ *   positions [T] int32, inv_freq [rot_dim / 2] fp64, both on the device
+ *            (unused, may be NULL, for rot_dim = 0)                   (read)
+ *   q_out [T, hq, d], k_out [T, hkv, d]   dtype, dense                (written)
+ * q_out may be q and k_out may be k where those are dense (any other overlap of
+ * inputs and outputs is undefined).  Sums in fp32, one rounding on the store. */
+MOBA_API moba_status_t moba_qk_norm_rope(const moba_rope_shape_t* shape, const void* q, const void* k,
+                                         const void* q_weight, const void* k_weight, const int32_t* positions,
+                                         const double* inv_freq, void* q_out, void* k_out, moba_stream_t stream);
+
+/* Device scratch bytes of moba_qk_norm_rope_bwd; 0 for an invalid shape. */
+MOBA_API size_t moba_qk_norm_rope_bwd_workspace_size(const moba_rope_shape_t* shape);
+
+/* Gradients of moba_qk_norm_rope.  With z the output's gradient rotated back
+ * and g = z w:  dx = r g - x r^3 <x, g> / d,  dw = sum over tokens and heads of
+ * z x r.
+ *   q, k, q_weight, k_weight, positions, inv_freq   as in the forward (read)
+ *   dq_out [T, hq, d], dk_out [T, hkv, d]   dtype, dense              (read)
+ *   dq [T, hq, d], dk [T, hkv, d]           dtype, dense              (written)
+ *   dq_weight, dk_weight [d]                weight_dtype              (written)
+ *   ws    >= moba_qk_norm_rope_bwd_workspace_size bytes of device scratch
+ * Sums in fp32 in a fixed order: results are bitwise reproducible.  dq may be
+ * dq_out and dk may be dk_out.  T = 0 writes zero weight gradients. */
+MOBA_API moba_status_t moba_qk_norm_rope_bwd(const moba_rope_shape_t* shape, const void* q, const void* k,
+                                             const void* q_weight, const void* k_weight, const int32_t* positions,
+                                             const double* inv_freq, const void* dq_out, const void* dk_out,
+                                             void* dq, void* dk, void* dq_weight, void* dk_weight, void* ws,
+                                             size_t ws_bytes, moba_stream_t stream);
+
+/* ---- paged key/value cache ------------------------------------------------- */
+
+/* The serving side of a layer: MoBA is used for prefill and full attention for
+ * generation ([summary] section 3, Implementation), and the last layers are
+ * full attention throughout.  Both read a cache that grows as tokens arrive.
+ *
+ * Pools k_pool, v_pool [num_pages, hkv, page_size, head_dim] (dtype) hold the
+ * keys and values of all sequences; position u of sequence b is slot
+ * u % page_size of page table[b, u / page_size].  A step brings T new tokens,
+ * the sequences' one after another:
+ *   cu_new [batch + 1] int32   sequence b's new tokens are the rows
+ *                              cu_new[b] .. cu_new[b + 1) (cu_new[0] = 0,
+ *                              non-decreasing; a sequence may have none).  Rows
+ *                              from cu_new[batch] on are padding: not read, and
+ *                              in the results left as they were.
+ *   kv_len [batch] int32       keys of the sequence, the new tokens INCLUDED:
+ *                              its new token i has position
+ *                              kv_len[b] - (its new tokens) + i
+ *   table  [batch, max_pages] int32   entries behind a sequence's last page
+ *                              are not read
+ * All three live on the device; no call reads them on the host, so a captured
+ * call can be replayed with other lengths and pages.
+ *
+ * An entry of the table outside [0, num_pages), or a length beyond max_pages
+ * pages, is not followed: *status (a device int32, or NULL) becomes
+ * MOBA_ERR_INTERNAL and the results of that sequence are not meaningful; nothing
+ * out of range is read or written.  Calls set *status on an error and
+ * never clear it.  Slots behind a sequence's length, and pages of no sequence,
+ * may hold anything, NaN included. */
+typedef struct {
+  int32_t batch;         /* sequences, 1 .. 65535                                  */
+  int32_t tokens;        /* T >= 0: rows of q, k, v                                */
+  int32_t hq, hkv;       /* heads; hq % hkv == 0                                   */
+  int32_t head_dim;      /* 64 or 128                                              */
+  int32_t page_size;     /* tokens a page: a power of two, 16 or more              */
+  int32_t num_pages;     /* pages of each pool                                     */
+  int32_t max_pages;     /* columns of the table                                   */
+  int32_t dtype;         /* moba_dtype_t of q, k, v, the pools and out             */
+  float scale;           /* softmax scale; <= 0 selects 1/sqrt(head_dim)           */
+  int64_t q_stride;      /* elements between tokens of q, k, v; 0 = dense.         */
+  int64_t k_stride;      /* Multiples of 16 bytes.                                 */
+  int64_t v_stride;
+  int64_t k_page_stride; /* elements between pages of the pools; 0 = dense         */
+  int64_t v_page_stride; /* (pages of one layer in an allocation of several)       */
+} moba_paged_shape_t;
+
+/* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31,
+ * max_pages * page_size < 2^31). */
+MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* shape);
+
+/* Appends the step's keys and values to the cache, keys (and queries, where
+ * given) normed and rotated on the way, each token at its position in its
+ * sequence; one kernel.
+ *   rope      rot_dim = 0: no rotation (inv_freq may be NULL)         (host)
+ *   q [T, hq, d] or NULL, k, v [T, hkv, d]   dtype                    (read)
+ *   q_weight, k_weight [d] weight_dtype; NULL: q, or k, is not normed (read)
+ *   inv_freq [rot_dim / 2] fp64, device                               (read)
+ *   q_out [T, hq, d] dtype, dense; NULL where q is; may be a dense q  (written)
+ *   k_pool, v_pool   the slots of the new tokens                      (written)
+ * Values are copied as they are.  Two sequences of a step must not append to
+ * one slot.  A token without a position or page (kv_len smaller than the new
+ * tokens, an entry out of range) is not written and sets *status. */
+MOBA_API moba_status_t moba_paged_append(const moba_paged_shape_t* shape, const moba_rope_t* rope, const void* q,
+                                         const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                         const double* inv_freq, const int32_t* cu_new, const int32_t* kv_len,
+                                         const int32_t* table, void* q_out, void* k_pool, void* v_pool, int* status,
+                                         moba_stream_t stream);
+
+/* Device scratch bytes of moba_paged_attn (a few ten MiB, whatever the lengths);
+ * 0 for an invalid shape. */
+MOBA_API size_t moba_paged_attn_workspace_size(const moba_paged_shape_t* shape);
+
+/* Causal attention of the new tokens over the cache (which holds them): the new
+ * token at position p attends the keys u <= p of its sequence,
+ *   z_u = scale <q, k_u>, out = sum softmax(z)_u v_u, lse = log sum exp z_u;
+ * query head h reads kv head h / (hq / hkv).  One new token a sequence is a
+ * decode step; any mix of lengths is one call.
+ *   q [T, hq, d]     dtype, token stride as in shape                  (read)
+ *   k_pool, v_pool   (read)
+ *   out [T, hq, d]   dtype, dense                                     (written)
+ *   lse [hq, T] fp32, natural log, or NULL                            (written)
+ *   ws    >= moba_paged_attn_workspace_size bytes of device scratch; calls that
+ *         overlap on the GPU need one each
+ * A row that sees no key (position < 0), or whose weights are all zero, gives
+ * out = 0 and lse = -infinity.  Keys and values that a row does not see do not
+ * reach it, infinities and NaN among them.  Results are bitwise reproducible.
+ * *status becomes MOBA_ERR_TIMEOUT if a bounded device-side wait of a
+ * tensor-core kernel expired (out is then invalid). */
+MOBA_API moba_status_t moba_paged_attn(const moba_paged_shape_t* shape, const void* q, const void* k_pool,
+                                       const void* v_pool, const int32_t* cu_new, const int32_t* kv_len,
+                                       const int32_t* table, void* out, float* lse, int* status, void* ws,
+                                       size_t ws_bytes, moba_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Static description of a status code. */

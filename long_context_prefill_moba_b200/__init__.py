@@ -18,7 +18,11 @@ three steps) and ``moba_forward`` (allocating convenience call), the backward
 (``moba_attn_bwd``, ``moba_attention``), the host-buffer layer
 (``moba_prefill_host``, ``MobaHostLayer``) and the gate variant with max- and
 min-pooled keys (``moba_block_maxminpool``, ``moba_gate_pooled``,
-``moba_attn_fwd_pooled``, ``MobaPooledLayer``, ``moba_forward_pooled``).
+``moba_attn_fwd_pooled``, ``MobaPooledLayer``, ``moba_forward_pooled``), the norm and
+rotation of queries and keys before the attention (``moba_qk_norm_rope``, its
+backward, ``moba_norm_rope`` as a differentiable op) and the paged cache of a
+serving step (``moba_paged_append``, ``moba_paged_attn``; with torch tensors
+``moba_cache_append``, ``moba_cache_attention``).
 """
 from __future__ import annotations
 
@@ -40,7 +44,11 @@ __all__ = [
     "moba_attn_bwd_workspace_size", "moba_attn_bwd", "moba_attention",
     "moba_pooled_wide_shape", "moba_block_maxminpool", "moba_gate_pooled", "moba_attn_fwd_pooled",
     "MobaPooledLayer", "moba_forward_pooled", "moba_workspace_size", "moba_rows_capacity",
-    "moba_check_index", "MOBA_BF16", "MOBA_F32", "EXPORTED_SYMBOLS",
+    "moba_check_index", "MobaRope", "MobaRopeShape", "MobaPagedShape", "make_rope_shape",
+    "make_paged_shape", "moba_check_rope_shape", "moba_check_paged_shape", "moba_rope_inv_freq",
+    "moba_qk_norm_rope", "moba_qk_norm_rope_bwd_workspace_size", "moba_qk_norm_rope_bwd",
+    "moba_norm_rope", "moba_paged_append", "moba_paged_attn_workspace_size", "moba_paged_attn",
+    "moba_cache_append", "moba_cache_attention", "MOBA_BF16", "MOBA_F32", "EXPORTED_SYMBOLS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,6 +67,9 @@ EXPORTED_SYMBOLS = [
     "moba_prefill_host_workspace_size", "moba_prefill_host", "moba_attn_bwd_workspace_size",
     "moba_attn_bwd", "moba_pooled_wide_shape", "moba_block_maxminpool", "moba_gate_pooled",
     "moba_attn_fwd_pooled", "moba_workspace_size", "moba_rows_capacity", "moba_check_index",
+    "moba_check_rope_shape", "moba_qk_norm_rope", "moba_qk_norm_rope_bwd_workspace_size",
+    "moba_qk_norm_rope_bwd", "moba_check_paged_shape", "moba_paged_append",
+    "moba_paged_attn_workspace_size", "moba_paged_attn",
 ]
 
 
@@ -72,6 +83,24 @@ class MobaShape(ctypes.Structure):
 
     def __repr__(self):
         return "MobaShape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class MobaRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class MobaRopeShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("rope", MobaRope)]
+
+
+class MobaPagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "tokens", "hq", "hkv", "head_dim", "page_size",
+                                              "num_pages", "max_pages", "dtype")] + [
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in (
+            "q_stride", "k_stride", "v_stride", "k_page_stride", "v_page_stride")]
 
 
 class MobaError(RuntimeError):
@@ -137,6 +166,23 @@ def load_library(path: str = LIB_PATH):
     L.moba_attn_fwd_pooled.restype = st
     L.moba_check_index.argtypes = [P, i32, vp, vp, vp, vp, vp]
     L.moba_check_index.restype = st
+    R, G, E = (ctypes.POINTER(t) for t in (MobaRopeShape, MobaPagedShape, MobaRope))
+    L.moba_check_rope_shape.argtypes = [R]
+    L.moba_check_rope_shape.restype = st
+    L.moba_qk_norm_rope.argtypes = [R] + [vp] * 9
+    L.moba_qk_norm_rope.restype = st
+    L.moba_qk_norm_rope_bwd_workspace_size.argtypes = [R]
+    L.moba_qk_norm_rope_bwd_workspace_size.restype = sz
+    L.moba_qk_norm_rope_bwd.argtypes = [R] + [vp] * 13 + [sz, vp]
+    L.moba_qk_norm_rope_bwd.restype = st
+    L.moba_check_paged_shape.argtypes = [G]
+    L.moba_check_paged_shape.restype = st
+    L.moba_paged_append.argtypes = [G, E] + [vp] * 14
+    L.moba_paged_append.restype = st
+    L.moba_paged_attn_workspace_size.argtypes = [G]
+    L.moba_paged_attn_workspace_size.restype = sz
+    L.moba_paged_attn.argtypes = [G] + [vp] * 10 + [sz, vp]
+    L.moba_paged_attn.restype = st
     L.moba_status_string.argtypes = [st]
     L.moba_status_string.restype = ctypes.c_char_p
     L.moba_last_cuda_error.argtypes = []
@@ -529,3 +575,259 @@ def moba_attention(q, k, v, block, topk, scale=None, query_chunk=0):
     """Differentiable MoBA attention: q [b,N,Hq,d], k/v [b,N,Hkv,d] CUDA tensors
     -> out [b,N,Hq,d]; gradients flow to q, k, v (not through the block selection)."""
     return _MobaAttention.apply(q, k, v, block, topk, scale, query_chunk)
+
+
+# ---- norm and rotation of queries and keys, paged cache ----------------------
+
+_DTYPES = {"bf16": MOBA_BF16, torch.bfloat16: MOBA_BF16, "f32": MOBA_F32, torch.float32: MOBA_F32}
+
+
+def make_rope_shape(tokens, hq, hkv, head_dim, rot_dim, dtype="bf16", weight_dtype=None, eps=1e-6,
+                    interleaved=False, q_stride=0, k_stride=0) -> MobaRopeShape:
+    dt = _DTYPES[dtype]
+    wt = dt if weight_dtype is None else _DTYPES[weight_dtype]
+    return MobaRopeShape(tokens, hq, hkv, head_dim, dt, q_stride, k_stride,
+                         MobaRope(rot_dim, 1 if interleaved else 0, wt, eps))
+
+
+def make_paged_shape(batch, tokens, hq, hkv, head_dim, page_size, num_pages, max_pages, dtype="bf16",
+                     scale=None, q_stride=0, k_stride=0, v_stride=0, k_page_stride=0,
+                     v_page_stride=0) -> MobaPagedShape:
+    return MobaPagedShape(batch, tokens, hq, hkv, head_dim, page_size, num_pages, max_pages, _DTYPES[dtype],
+                          0.0 if scale is None else float(scale), q_stride, k_stride, v_stride,
+                          k_page_stride, v_page_stride)
+
+
+def moba_check_rope_shape(shape) -> int: return lib().moba_check_rope_shape(_s(shape))
+def moba_check_paged_shape(shape) -> int: return lib().moba_check_paged_shape(_s(shape))
+
+
+def moba_qk_norm_rope_bwd_workspace_size(shape) -> int:
+    return lib().moba_qk_norm_rope_bwd_workspace_size(_s(shape))
+
+
+def moba_paged_attn_workspace_size(shape) -> int:
+    return lib().moba_paged_attn_workspace_size(_s(shape))
+
+
+def _at(t):
+    # a tensor whose strides the shape carries
+    return None if t is None else t.data_ptr()
+
+
+def moba_qk_norm_rope(shape, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream=None):
+    """q and k may be strided rows (shape.q_stride, shape.k_stride)."""
+    _check(lib().moba_qk_norm_rope(_s(shape), _at(q), _at(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                                   _ptr(inv_freq), _ptr(q_out), _ptr(k_out), _stream(stream)),
+           "moba_qk_norm_rope")
+
+
+def moba_qk_norm_rope_bwd(shape, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk,
+                          dq_weight, dk_weight, ws, stream=None):
+    _check(lib().moba_qk_norm_rope_bwd(_s(shape), _at(q), _at(k), _ptr(q_weight), _ptr(k_weight),
+                                       _ptr(positions), _ptr(inv_freq), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
+                                       _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(ws),
+                                       ws.numel() * ws.element_size(), _stream(stream)),
+           "moba_qk_norm_rope_bwd")
+
+
+def moba_paged_append(shape, rope, q, k, v, q_weight, k_weight, inv_freq, cu_new, kv_len, table, q_out, k_pool,
+                      v_pool, status=None, stream=None):
+    """q, k, v and the pools may be strided (the strides are the shape's)."""
+    _check(lib().moba_paged_append(_s(shape), ctypes.byref(rope), _at(q), _at(k), _at(v), _ptr(q_weight),
+                                   _ptr(k_weight), _ptr(inv_freq), _ptr(cu_new), _ptr(kv_len), _ptr(table),
+                                   _ptr(q_out), _at(k_pool), _at(v_pool), _ptr(status), _stream(stream)),
+           "moba_paged_append")
+
+
+def moba_paged_attn(shape, q, k_pool, v_pool, cu_new, kv_len, table, out, lse, ws, status=None, stream=None):
+    """q and the pools may be strided (the strides are the shape's)."""
+    _check(lib().moba_paged_attn(_s(shape), _at(q), _at(k_pool), _at(v_pool), _ptr(cu_new), _ptr(kv_len),
+                                 _ptr(table), _ptr(out), _ptr(lse), _ptr(status), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)),
+           "moba_paged_attn")
+
+
+def moba_rope_inv_freq(rot_dim, theta=10000.0, device="cuda"):
+    """The rotation's frequencies theta^(-2i / rot_dim), fp64 [rot_dim / 2]."""
+    return theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+
+
+def _require(ok, where, what):
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _rows(x, where, name):
+    """x [..., h, d] and the elements between its tokens: as it is where its rows
+    lie one stride apart (part of a fused projection), else a dense copy."""
+    _require(x.dim() >= 3 and x.is_cuda, where, f"{name} must be a CUDA tensor [..., heads, head_dim]")
+    h, d = x.shape[-2:]
+    st = x.stride()
+    step = st[-3]
+    if (st[-1] == 1 and (h == 1 or st[-2] == d) and step >= h * d and step * x.element_size() % 16 == 0
+            and all(x.shape[i] == 1 or st[i] == st[i + 1] * x.shape[i + 1] for i in range(x.dim() - 3))):
+        return x, step
+    return x.contiguous(), h * d
+
+
+def _on(x):
+    """x's device made the current one (the library launches on the current device)."""
+    return torch.cuda.device(x.device)
+
+
+def _same(where, ref, dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            _require(t.dtype == dtype and t.device == ref.device, where,
+                     f"{name} must be {dtype} on {ref.device}, not {t.dtype} on {t.device}")
+
+
+def _norm_rope_shape(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+    where = "moba_norm_rope"
+    q, qs = _rows(q, where, "q")
+    k, ks = _rows(k, where, "k")
+    _require(q.dtype in _DTYPES and q_weight.dtype in _DTYPES, where, "bf16 or fp32 tensors")
+    _same(where, q, q.dtype, k=k)
+    _same(where, q, q_weight.dtype, q_weight=q_weight, k_weight=k_weight)
+    _same(where, q, torch.int32, positions=positions)
+    _same(where, q, torch.float64, inv_freq=inv_freq)
+    hq, d = q.shape[-2:]
+    _require(k.shape[:-2] == q.shape[:-2] and k.shape[-1] == d, where, "q and k must hold the same tokens and head_dim")
+    _require(q_weight.shape == (d,) and k_weight.shape == (d,), where, "the weights must be [head_dim]")
+    tokens = q.numel() // (hq * d)
+    _require(positions.numel() == tokens, where, "one position a token")
+    shape = make_rope_shape(tokens, hq, k.shape[-2], d, 2 * inv_freq.numel(), q.dtype, q_weight.dtype, eps,
+                            interleaved, qs, ks)
+    return q, k, shape
+
+
+class _MobaNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+        q, k, shape = _norm_rope_shape(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        with _on(q):
+            moba_qk_norm_rope(shape, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+        ctx.shape = shape
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        return q_out, k_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dqw, dkw = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        with _on(q):
+            ws = torch.empty(moba_qk_norm_rope_bwd_workspace_size(ctx.shape), dtype=torch.uint8, device=q.device)
+            moba_qk_norm_rope_bwd(ctx.shape, q, k, q_weight, k_weight, positions, inv_freq, dq_out.contiguous(),
+                                  dk_out.contiguous(), dq, dk, dqw, dkw, ws)
+        return dq, dk, dqw, dkw, None, None, None, None
+
+
+def moba_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False):
+    """Norm of every query and key head and the position rotation, in one pass and
+    differentiable in q, k and the weights: what precedes moba_attention in a layer.
+
+    q [..., Hq, d], k [..., Hkv, d] with the same leading dimensions (rows of a fused
+    projection are read where they lie), q_weight/k_weight [d], positions int32 with
+    one entry a token, inv_freq fp64 [rot_dim / 2] (moba_rope_inv_freq).  Returns
+    (q_out, k_out), dense.  Runs on the current stream of q's device.  A step captured
+    into a CUDA graph with its backward needs every earlier autograd graph of the same
+    leaves freed first (torch ties a leaf's gradient node to the stream it was made on)."""
+    q_weight, k_weight, positions, inv_freq = (x.contiguous() for x in (q_weight, k_weight, positions, inv_freq))
+    if torch.is_grad_enabled() and any(x.requires_grad for x in (q, k, q_weight, k_weight)):
+        return _MobaNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    q, k, shape = _norm_rope_shape(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    with _on(q):
+        moba_qk_norm_rope(shape, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    return q_out, k_out
+
+
+def _paged_shape(where, ref, hq, k_pool, v_pool, cu_new, kv_len, table, status, tokens, scale=None, strides=(0, 0, 0)):
+    _require(k_pool.dim() == 4 and k_pool.shape == v_pool.shape, where,
+             "the pools must be [num_pages, heads, page_size, head_dim], alike")
+    pages, hkv, page, d = k_pool.shape
+    _require(ref.dtype in _DTYPES, where, "bf16 or fp32 tensors")
+    for name, p in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _require(p.stride()[1:] == (page * d, d, 1), where, f"a page of {name} must be dense")
+    _same(where, ref, ref.dtype, k_pool=k_pool, v_pool=v_pool)
+    _same(where, ref, torch.int32, cu_new=cu_new, kv_len=kv_len, table=table, status=status)
+    _require(table.dim() == 2 and kv_len.shape == (table.shape[0],) and cu_new.shape == (table.shape[0] + 1,), where,
+             "table must be [batch, max_pages], kv_len [batch], cu_new [batch + 1]")
+    _require(ref.shape[-1] == d and hq % hkv == 0, where, "the heads must match the pools'")
+    return make_paged_shape(table.shape[0], tokens, hq, hkv, d, page, pages, table.shape[1], ref.dtype, scale, *strides,
+                            k_pool.stride(0) if pages > 1 else 0, v_pool.stride(0) if pages > 1 else 0)
+
+
+def moba_cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq=None, q=None, q_weight=None,
+                      k_weight=None, eps=1e-6, interleaved=False, status=None, q_out=None):
+    """Append a step's keys and values to the paged cache; keys, and queries where
+    given, are normed (with weights) and rotated (with inv_freq) on the way.
+
+    k, v [T, Hkv, d], q [T, Hq, d] (rows of a fused projection are read where they
+    lie); k_pool, v_pool [num_pages, Hkv, page_size, d]; cu_new int32 [batch + 1], kv_len
+    int32 [batch] (new tokens included), table int32 [batch, max_pages].  `status`: a
+    zeroed int32 CUDA tensor that becomes nonzero if a token had no page.  Returns the
+    queries (None without q): q_out, or a new tensor whose rows from cu_new[-1] on
+    are not written.  Runs on the current stream of k's device."""
+    where = "moba_cache_append"
+    k, ks = _rows(k, where, "k")
+    v, vs = _rows(v, where, "v")
+    _require(k.dim() == 3 and k.shape == v.shape and k.shape[1:] == k_pool.shape[1::2], where,
+             "k and v must be [tokens, heads, head_dim] with the pools' heads")
+    _same(where, k, k.dtype, v=v, q=q, q_out=q_out)
+    qs = 0
+    if q is not None:
+        q, qs = _rows(q, where, "q")
+        _require(q.dim() == 3 and q.shape[0] == k.shape[0], where, "q must hold the same tokens as k")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _require(q_out.shape == q.shape, where, "q_out must have q's shape")
+    _require(q is not None or (q_weight is None and q_out is None), where, "q_weight and q_out go with q")
+    weight = q_weight if q_weight is not None else k_weight
+    _require(weight is None or weight.dtype in _DTYPES, where, "bf16 or fp32 weights")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _same(where, k, weight.dtype, **{name: w})
+            _require(w.shape == k.shape[-1:], where, "the weights must be [head_dim]")
+    _same(where, k, torch.float64, inv_freq=inv_freq)
+    shape = _paged_shape(where, k, k.shape[1] if q is None else q.shape[1], k_pool, v_pool, cu_new, kv_len, table,
+                         status, k.shape[0], None, (qs, ks, vs))
+    rope = MobaRope(0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
+                    MOBA_BF16 if weight is None else _DTYPES[weight.dtype], eps)
+    with _on(k):
+        moba_paged_append(shape, rope, q, k, v, q_weight, k_weight, inv_freq, cu_new, kv_len, table, q_out, k_pool,
+                          v_pool, status)
+    return q_out
+
+
+def moba_cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale=None, return_lse=False, out=None, status=None):
+    """Causal attention of a step's new tokens over the paged cache that holds them
+    (moba_cache_append): one token a sequence is a decode step, any mix of lengths
+    one call.
+
+    q [T, Hq, d]; the other arguments as for moba_cache_append.  Returns out [T, Hq, d],
+    with return_lse also the log-sum-exp [Hq, T] in fp32; rows from cu_new[-1] on are
+    not written.  The workspace comes from torch's allocator, so that calls on
+    several streams, and captured graphs, have one each.  Runs on the current stream
+    of q's device."""
+    where = "moba_cache_attention"
+    q, qs = _rows(q, where, "q")
+    _require(q.dim() == 3, where, "q must be [tokens, heads, head_dim]")
+    shape = _paged_shape(where, q, q.shape[1], k_pool, v_pool, cu_new, kv_len, table, status, q.shape[0], scale,
+                         (qs, 0, 0))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _same(where, q, q.dtype, out=out)
+    _require(out.shape == q.shape, where, "out must have q's shape")
+    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device) if return_lse else None
+    with _on(q):
+        ws = torch.empty(moba_paged_attn_workspace_size(shape), dtype=torch.uint8, device=q.device)
+        moba_paged_attn(shape, q, k_pool, v_pool, cu_new, kv_len, table, out, lse, ws, status)
+    return (out, lse) if return_lse else out

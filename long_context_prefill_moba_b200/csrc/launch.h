@@ -116,6 +116,47 @@ cudaError_t launch_index_check(const Dims& dm, int exact, int32_t* sel, int32_t*
                                const int32_t* rows, int64_t capacity, int* status, cudaStream_t stream,
                                int* launches);
 
+// per-head norm and position rotation (norm_rope.cu).  The backward reads q, k
+// (the forward's inputs) and writes the gradients to q_out, k_out.
+struct RopeArgs {
+  const void *q, *k, *v;            // rows of q_stride / k_stride / v_stride elements (v: append only)
+  void *q_out, *k_out, *v_out;      // dense; k_out, v_out are the pools for the append
+  const void *q_weight, *k_weight;  // [d], or null: no norm
+  const int32_t* positions;
+  const double* inv_freq;           // [rot / 2]
+  int tokens, hq, hkv, rot, interleaved, weight_f32;
+  float eps;
+  int64_t q_stride, k_stride, v_stride;
+  int split;                        // warps a token (set by the launcher)
+  // append
+  const int32_t *cu, *kv_len, *table;
+  int batch, page_shift, max_pages, num_pages;
+  int64_t k_page_stride, v_page_stride;
+  int* status;
+};
+cudaError_t launch_norm_rope(const RopeArgs& a, int dtype, int d, bool append, cudaStream_t stream, int* launches);
+size_t norm_rope_bwd_ws(int d);
+cudaError_t launch_norm_rope_bwd(const RopeArgs& a, int dtype, int d, const void* dq_out, const void* dk_out, void* dqw,
+                                 void* dkw, float* part, cudaStream_t stream, int* launches);
+
+// attention of new tokens over a paged cache (paged_attn.cu)
+struct PagedDims {
+  int batch, tokens, hq, hkv, G, page_shift, max_pages, num_pages;
+  int64_t q_stride;                      // elements between tokens of q
+  int64_t k_page_stride, v_page_stride;  // elements between pages
+  float scale_log2;
+};
+struct PagedArgs {
+  const void *q, *k_pool, *v_pool;
+  const int32_t *cu, *kv_len, *table;
+  void* out;
+  float* lse;    // [hq, tokens] or null
+  int* status;   // or null
+};
+size_t paged_attn_ws(int dtype, int d);
+cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const PagedArgs& a, void* ws, cudaStream_t stream,
+                              int* launches);
+
 // a kernel whose only wait can never complete: it must time out (status word)
 cudaError_t launch_bounded_wait_selftest(int* status, cudaStream_t stream);
 

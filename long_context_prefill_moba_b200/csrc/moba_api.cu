@@ -16,6 +16,7 @@ constexpr int64_t kPartialBudget = 8ll << 30;   // bytes of partials per pass (a
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int64_t nblocks(const moba_shape_t* s) { return ((int64_t)s->seqlen + s->block - 1) / s->block; }
@@ -122,6 +123,49 @@ moba_status_t finish(cudaError_t e, int launches) {
     return MOBA_ERR_CUDA;
   }
   return MOBA_OK;
+}
+
+// ---- serving entry points: rotation, paged cache ------------------------------
+bool dtype_ok(int t) { return t == MOBA_BF16 || t == MOBA_F32; }
+int64_t elem_bytes(int t) { return t == MOBA_BF16 ? 2 : 4; }
+// a row stride in elements: 0 selects dense rows; rows must not overlap and
+// must start on 16-byte boundaries
+bool stride_ok(int64_t stride, int64_t dense, int64_t es) {
+  return stride == 0 || (stride >= dense && stride * es % 16 == 0);
+}
+
+moba_status_t check_rope(const moba_rope_t* r, int head_dim) {
+  if (r->rot_dim < 0 || r->rot_dim > head_dim || (r->interleaved != 0 && r->interleaved != 1)) return MOBA_ERR_INVALID_ARG;
+  if (!dtype_ok(r->weight_dtype)) return MOBA_ERR_INVALID_ARG;
+  if (!(r->eps >= 0.f) || isinf(r->eps)) return MOBA_ERR_INVALID_ARG;
+  if (r->rot_dim % 16 != 0) return MOBA_ERR_UNSUPPORTED;
+  return MOBA_OK;
+}
+
+moba::RopeArgs rope_args(const moba_rope_t* r) {
+  moba::RopeArgs a = {};
+  a.rot = r->rot_dim;
+  a.interleaved = r->interleaved;
+  a.weight_f32 = r->weight_dtype == MOBA_F32;
+  a.eps = r->eps;
+  a.split = 1;
+  return a;
+}
+moba::RopeArgs rope_shape_args(const moba_rope_shape_t* s) {
+  moba::RopeArgs a = rope_args(&s->rope);
+  a.tokens = s->tokens;
+  a.hq = s->hq;
+  a.hkv = s->hkv;
+  a.q_stride = s->q_stride > 0 ? s->q_stride : (int64_t)s->hq * s->head_dim;
+  a.k_stride = s->k_stride > 0 ? s->k_stride : (int64_t)s->hkv * s->head_dim;
+  return a;
+}
+
+int64_t page_dense(const moba_paged_shape_t* s) { return (int64_t)s->hkv * s->page_size * s->head_dim; }
+int page_shift(const moba_paged_shape_t* s) {
+  int sh = 0;
+  while ((1 << sh) < s->page_size) ++sh;
+  return sh;
 }
 
 }  // namespace
@@ -588,5 +632,166 @@ MOBA_API moba_status_t moba_selftest_bounded_wait(int* status, moba_stream_t str
 
 MOBA_API int moba_last_cuda_error(void) { return g_last_cuda_error; }
 MOBA_API int moba_last_launch_count(void) { return g_last_launches; }
+
+// ---- norm and rotation, paged cache ---------------------------------------------
+
+MOBA_API moba_status_t moba_check_rope_shape(const moba_rope_shape_t* s) {
+  if (s == nullptr) return MOBA_ERR_INVALID_ARG;
+  if (s->tokens < 0 || s->hq < 1 || s->hkv < 1 || s->head_dim < 1 || s->hq % s->hkv != 0 || !dtype_ok(s->dtype))
+    return MOBA_ERR_INVALID_ARG;
+  if (s->head_dim != 64 && s->head_dim != 128) return MOBA_ERR_UNSUPPORTED;
+  const int64_t es = elem_bytes(s->dtype);
+  if (!stride_ok(s->q_stride, (int64_t)s->hq * s->head_dim, es) ||
+      !stride_ok(s->k_stride, (int64_t)s->hkv * s->head_dim, es))
+    return MOBA_ERR_INVALID_ARG;
+  const moba_status_t st = check_rope(&s->rope, s->head_dim);
+  if (st != MOBA_OK) return st;
+  if ((int64_t)s->tokens * s->hq > kI32Max) return MOBA_ERR_UNSUPPORTED;
+  return MOBA_OK;
+}
+
+MOBA_API moba_status_t moba_qk_norm_rope(const moba_rope_shape_t* s, const void* q, const void* k, const void* q_weight,
+                                         const void* k_weight, const int32_t* positions, const double* inv_freq,
+                                         void* q_out, void* k_out, moba_stream_t stream) {
+  g_last_launches = 0;
+  moba_status_t st = moba_check_rope_shape(s);
+  if (st != MOBA_OK) return st;
+  if (s->tokens == 0) return MOBA_OK;
+  const bool rot = s->rope.rot_dim > 0;
+  if (q == nullptr || k == nullptr || q_weight == nullptr || k_weight == nullptr || q_out == nullptr || k_out == nullptr ||
+      (rot && (positions == nullptr || inv_freq == nullptr)))
+    return MOBA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(q_out) ||
+      !aligned16(k_out) || !aligned4(positions) || !aligned8(inv_freq))
+    return MOBA_ERR_INVALID_ARG;
+  moba::RopeArgs a = rope_shape_args(s);
+  // in place only where a row's results land on the row
+  if ((q_out == q && a.q_stride != (int64_t)s->hq * s->head_dim) || (k_out == k && a.k_stride != (int64_t)s->hkv * s->head_dim))
+    return MOBA_ERR_INVALID_ARG;
+  a.q = q; a.k = k; a.q_weight = q_weight; a.k_weight = k_weight;
+  a.positions = positions; a.inv_freq = inv_freq;
+  a.q_out = q_out; a.k_out = k_out;
+  int launches = 0;
+  return finish(moba::launch_norm_rope(a, s->dtype, s->head_dim, false, (cudaStream_t)stream, &launches), launches);
+}
+
+MOBA_API size_t moba_qk_norm_rope_bwd_workspace_size(const moba_rope_shape_t* s) {
+  return moba_check_rope_shape(s) == MOBA_OK ? align_up(moba::norm_rope_bwd_ws(s->head_dim)) : 0;
+}
+
+MOBA_API moba_status_t moba_qk_norm_rope_bwd(const moba_rope_shape_t* s, const void* q, const void* k,
+                                             const void* q_weight, const void* k_weight, const int32_t* positions,
+                                             const double* inv_freq, const void* dq_out, const void* dk_out, void* dq,
+                                             void* dk, void* dq_weight, void* dk_weight, void* ws, size_t ws_bytes,
+                                             moba_stream_t stream) {
+  g_last_launches = 0;
+  moba_status_t st = moba_check_rope_shape(s);
+  if (st != MOBA_OK) return st;
+  const bool rot = s->rope.rot_dim > 0, any = s->tokens > 0;
+  if (q_weight == nullptr || k_weight == nullptr || dq_weight == nullptr || dk_weight == nullptr || ws == nullptr ||
+      (any && (q == nullptr || k == nullptr || dq_out == nullptr || dk_out == nullptr || dq == nullptr || dk == nullptr)) ||
+      (any && rot && (positions == nullptr || inv_freq == nullptr)))
+    return MOBA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(dq_out) ||
+      !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dq_weight) || !aligned16(dk_weight) ||
+      !aligned16(ws) || !aligned4(positions) || !aligned8(inv_freq))
+    return MOBA_ERR_INVALID_ARG;
+  if (ws_bytes < moba_qk_norm_rope_bwd_workspace_size(s)) return MOBA_ERR_WORKSPACE;
+  moba::RopeArgs a = rope_shape_args(s);
+  a.q = q; a.k = k; a.q_weight = q_weight; a.k_weight = k_weight;
+  a.positions = positions; a.inv_freq = inv_freq;
+  a.q_out = dq; a.k_out = dk;
+  int launches = 0;
+  return finish(moba::launch_norm_rope_bwd(a, s->dtype, s->head_dim, dq_out, dk_out, dq_weight, dk_weight, (float*)ws,
+                                           (cudaStream_t)stream, &launches),
+                launches);
+}
+
+MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* s) {
+  if (s == nullptr) return MOBA_ERR_INVALID_ARG;
+  if (s->batch < 1 || s->tokens < 0 || s->hq < 1 || s->hkv < 1 || s->head_dim < 1 || s->page_size < 1 ||
+      s->num_pages < 1 || s->max_pages < 1 || s->hq % s->hkv != 0 || !dtype_ok(s->dtype))
+    return MOBA_ERR_INVALID_ARG;
+  if (isnan(s->scale) || isinf(s->scale)) return MOBA_ERR_INVALID_ARG;
+  if (s->head_dim != 64 && s->head_dim != 128) return MOBA_ERR_UNSUPPORTED;
+  if (s->page_size < 16 || (s->page_size & (s->page_size - 1)) != 0) return MOBA_ERR_UNSUPPORTED;
+  const int64_t es = elem_bytes(s->dtype), kv = (int64_t)s->hkv * s->head_dim;
+  if (!stride_ok(s->q_stride, (int64_t)s->hq * s->head_dim, es) || !stride_ok(s->k_stride, kv, es) ||
+      !stride_ok(s->v_stride, kv, es) || !stride_ok(s->k_page_stride, page_dense(s), es) ||
+      !stride_ok(s->v_page_stride, page_dense(s), es))
+    return MOBA_ERR_INVALID_ARG;
+  if (s->batch > kGridYZMax || (int64_t)s->tokens * s->hq > kI32Max ||
+      (int64_t)s->max_pages * s->page_size > kI32Max)
+    return MOBA_ERR_UNSUPPORTED;
+  return MOBA_OK;
+}
+
+MOBA_API moba_status_t moba_paged_append(const moba_paged_shape_t* s, const moba_rope_t* rope, const void* q,
+                                         const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                         const double* inv_freq, const int32_t* cu_new, const int32_t* kv_len,
+                                         const int32_t* table, void* q_out, void* k_pool, void* v_pool, int* status,
+                                         moba_stream_t stream) {
+  g_last_launches = 0;
+  moba_status_t st = moba_check_paged_shape(s);
+  if (st != MOBA_OK) return st;
+  if (rope == nullptr) return MOBA_ERR_INVALID_ARG;
+  if ((st = check_rope(rope, s->head_dim)) != MOBA_OK) return st;
+  if (s->tokens == 0) return MOBA_OK;
+  if (k == nullptr || v == nullptr || k_pool == nullptr || v_pool == nullptr || cu_new == nullptr || kv_len == nullptr ||
+      table == nullptr || (rope->rot_dim > 0 && inv_freq == nullptr))
+    return MOBA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr && q_weight != nullptr)) return MOBA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned4(cu_new) || !aligned4(kv_len) ||
+      !aligned4(table) || !aligned4(status) || !aligned8(inv_freq))
+    return MOBA_ERR_INVALID_ARG;
+  moba::RopeArgs a = rope_args(rope);
+  const int64_t kv = (int64_t)s->hkv * s->head_dim;
+  a.tokens = s->tokens; a.hq = s->hq; a.hkv = s->hkv;
+  a.q_stride = s->q_stride > 0 ? s->q_stride : (int64_t)s->hq * s->head_dim;
+  a.k_stride = s->k_stride > 0 ? s->k_stride : kv;
+  a.v_stride = s->v_stride > 0 ? s->v_stride : kv;
+  if (q != nullptr && q_out == q && a.q_stride != (int64_t)s->hq * s->head_dim) return MOBA_ERR_INVALID_ARG;
+  a.q = q; a.k = k; a.v = v; a.q_weight = q_weight; a.k_weight = k_weight; a.inv_freq = inv_freq;
+  a.q_out = q_out; a.k_out = k_pool; a.v_out = v_pool;
+  a.cu = cu_new; a.kv_len = kv_len; a.table = table;
+  a.batch = s->batch; a.page_shift = page_shift(s); a.max_pages = s->max_pages; a.num_pages = s->num_pages;
+  a.k_page_stride = s->k_page_stride > 0 ? s->k_page_stride : page_dense(s);
+  a.v_page_stride = s->v_page_stride > 0 ? s->v_page_stride : page_dense(s);
+  a.status = status;
+  int launches = 0;
+  return finish(moba::launch_norm_rope(a, s->dtype, s->head_dim, true, (cudaStream_t)stream, &launches), launches);
+}
+
+MOBA_API size_t moba_paged_attn_workspace_size(const moba_paged_shape_t* s) {
+  return moba_check_paged_shape(s) == MOBA_OK ? align_up(moba::paged_attn_ws(s->dtype, s->head_dim)) : 0;
+}
+
+MOBA_API moba_status_t moba_paged_attn(const moba_paged_shape_t* s, const void* q, const void* k_pool, const void* v_pool,
+                                       const int32_t* cu_new, const int32_t* kv_len, const int32_t* table, void* out,
+                                       float* lse, int* status, void* ws, size_t ws_bytes, moba_stream_t stream) {
+  g_last_launches = 0;
+  moba_status_t st = moba_check_paged_shape(s);
+  if (st != MOBA_OK) return st;
+  if (s->tokens == 0) return MOBA_OK;
+  if (q == nullptr || k_pool == nullptr || v_pool == nullptr || cu_new == nullptr || kv_len == nullptr || table == nullptr ||
+      out == nullptr || ws == nullptr)
+    return MOBA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(ws) || !aligned4(cu_new) ||
+      !aligned4(kv_len) || !aligned4(table) || !aligned4(lse) || !aligned4(status))
+    return MOBA_ERR_INVALID_ARG;
+  if (ws_bytes < moba_paged_attn_workspace_size(s)) return MOBA_ERR_WORKSPACE;
+  moba::PagedDims dm;
+  dm.batch = s->batch; dm.tokens = s->tokens; dm.hq = s->hq; dm.hkv = s->hkv; dm.G = s->hq / s->hkv;
+  dm.page_shift = page_shift(s); dm.max_pages = s->max_pages; dm.num_pages = s->num_pages;
+  dm.q_stride = s->q_stride > 0 ? s->q_stride : (int64_t)s->hq * s->head_dim;
+  dm.k_page_stride = s->k_page_stride > 0 ? s->k_page_stride : page_dense(s);
+  dm.v_page_stride = s->v_page_stride > 0 ? s->v_page_stride : page_dense(s);
+  const float scale = s->scale > 0.f ? s->scale : 1.0f / sqrtf((float)s->head_dim);
+  dm.scale_log2 = scale * moba::kLog2e;
+  moba::PagedArgs a = {q, k_pool, v_pool, cu_new, kv_len, table, out, lse, status};
+  int launches = 0;
+  return finish(moba::launch_paged_attn(dm, s->dtype, s->head_dim, a, ws, (cudaStream_t)stream, &launches), launches);
+}
 
 }  // extern "C"

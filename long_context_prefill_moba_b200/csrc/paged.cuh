@@ -1,0 +1,158 @@
+// Work division shared by the kernels of the attention over a paged cache.
+//
+// An item is one kv head of one sequence and `BR` of its rows (row i: new token
+// i / G, query head i % G of the group), with the key tiles (BK keys each) that
+// its last row may see.  The items of a call, in the order sequence, head, row
+// tile, form one line of W key tiles; worker w of E takes tiles [w W / E,
+// (w+1) W / E) of it, so that every worker has the same number of tiles (+- 1)
+// whatever the lengths are, and no host knowledge of them is needed.  An item
+// cut by a worker's border leaves fp32 partial results (at most two cut items
+// a worker: slot 2w the one it continues, slot 2w + 1 the one it begins), which
+// the combine kernel joins; the others are written by their worker.
+#pragma once
+
+#include "launch.h"
+
+namespace moba {
+
+struct PagedSeq {
+  int first;   // row of its first new token
+  int n;       // new tokens
+  int len;     // keys, new tokens included
+};
+
+MOBA_DEV PagedSeq paged_seq(const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len, const PagedDims& dm,
+                            int b) {
+  PagedSeq s;
+  s.first = min(max(cu[b], 0), dm.tokens);
+  s.n = max(min(cu[b + 1], dm.tokens) - s.first, 0);
+  // a length that the table's row cannot hold is cut to it (the status word says so)
+  const int64_t cap = (int64_t)dm.max_pages << dm.page_shift;
+  s.len = (int)min((int64_t)max(kv_len[b], 0), cap);
+  return s;
+}
+
+// keys that the row tile [rt BR, ..) may see, in tiles; one tile at least, so
+// that rows that see nothing are written too
+template <int BR, int BK>
+MOBA_DEV int paged_tiles(const PagedSeq& s, int G, int rt) {
+  const int64_t end = min((int64_t)s.n * G, (int64_t)(rt + 1) * BR);
+  const int last = (int)((end - 1) / G);
+  const int keys = max(s.len - s.n + last + 1, 0);
+  return max((keys + BK - 1) / BK, 1);
+}
+template <int BR>
+MOBA_DEV int paged_row_tiles(const PagedSeq& s, int G) { return (int)(((int64_t)s.n * G + BR - 1) / BR); }
+
+// tiles of one kv head of a sequence
+template <int BR, int BK>
+MOBA_DEV int64_t paged_head_tiles(const PagedSeq& s, int G) {
+  const int nrt = paged_row_tiles<BR>(s, G);
+  int64_t w = 0;
+  for (int rt = 0; rt < nrt; ++rt) w += paged_tiles<BR, BK>(s, G, rt);
+  return w;
+}
+
+template <int NT>
+struct PagedPlan {
+  int64_t before[NT + 1];   // tiles before the sequences of thread t
+  int64_t warp_sum[NT / 32];
+};
+
+// Whole block of NT threads: fills the plan, returns W.
+template <int BR, int BK, int NT>
+MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
+                            const PagedDims& dm) {
+  const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x, lane = t & 31;
+  int64_t w = 0;
+  for (int b = t * per; b < min((t + 1) * per, dm.batch); ++b)
+    w += paged_head_tiles<BR, BK>(paged_seq(cu, kv_len, dm, b), dm.G) * dm.hkv;
+  int64_t inc = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) p.warp_sum[t >> 5] = inc;
+  __syncthreads();
+  int64_t base = 0;
+  for (int i = 0; i < (t >> 5); ++i) base += p.warp_sum[i];
+  p.before[t] = base + inc - w;
+  if (t == NT - 1) p.before[NT] = base + inc;
+  __syncthreads();
+  return p.before[NT];
+}
+
+struct PagedItem {
+  int b, h, rt;
+  int tile, tiles;   // the position in it, and its key tiles
+  PagedSeq s;
+};
+
+// the item that holds tile `at` of the line (at < W)
+template <int BR, int BK, int NT>
+MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_t* __restrict__ cu,
+                                const int32_t* __restrict__ kv_len, const PagedDims& dm) {
+  const int per = (dm.batch + NT - 1) / NT;
+  int lo = 0, hi = NT - 1;   // the last thread whose sequences begin at or before `at`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.before[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  PagedItem it;
+  int64_t off = at - p.before[lo], head = 0;
+  it.b = lo * per;
+  for (;; ++it.b) {
+    it.s = paged_seq(cu, kv_len, dm, it.b);
+    head = paged_head_tiles<BR, BK>(it.s, dm.G);
+    if (off < head * dm.hkv || it.b + 1 >= dm.batch) break;
+    off -= head * dm.hkv;
+  }
+  it.h = (int)(off / head);
+  off -= it.h * head;
+  for (it.rt = 0;; ++it.rt) {
+    it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+    if (off < it.tiles) break;
+    off -= it.tiles;
+  }
+  it.tile = (int)off;
+  return it;
+}
+
+// the item after a finished one; call only while tiles of the line are left
+template <int BR, int BK>
+MOBA_DEV void paged_next(PagedItem& it, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
+                         const PagedDims& dm) {
+  it.tile = 0;
+  if (++it.rt >= paged_row_tiles<BR>(it.s, dm.G)) {
+    it.rt = 0;
+    if (++it.h >= dm.hkv) {
+      it.h = 0;
+      do {
+        ++it.b;
+        it.s = paged_seq(cu, kv_len, dm, it.b);
+      } while (it.s.n == 0 && it.b + 1 < dm.batch);
+    }
+  }
+  it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+}
+
+// Workspace of a call: E headers, then the partial results.
+struct PagedHeader {
+  int parts;       // workers the item is spread over if this worker begins it, else 0
+  int first, h, row0, rows;
+  int pad[3];
+};
+
+// parts of the item that worker w begins at tile `at` of the line and that ends
+// at tile `end`: the workers whose ranges reach into [at, end)
+MOBA_DEV int paged_parts(int64_t end, int64_t W, int64_t E, int64_t w) {
+  // the last worker v with v W / E < end
+  int64_t v = (end * E + W - 1) / W;
+  if (v > E) v = E;
+  while (v > 0 && (v - 1) * W / E >= end) --v;
+  while (v < E && v * W / E < end) ++v;
+  return (int)(v - w);
+}
+
+}  // namespace moba

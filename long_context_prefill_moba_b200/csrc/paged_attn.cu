@@ -1,0 +1,392 @@
+// Attention of new tokens over a paged cache, on CUDA cores, and the combine
+// kernel that joins the parts of an item (paged.cuh).
+//
+// For a row at position p with keys u <= p:  z_u = scale <q, k_u>,
+//   m = max z, l = sum 2^(z - m), o = sum 2^(z - m) v_u / l, lse = m + log l
+// in one pass over the keys with a running (m, l, o); z in units of log2(e).
+// A row that sees no key gives o = 0, lse = -inf.
+#include "paged.cuh"
+
+namespace moba {
+
+// ---- combine ---------------------------------------------------------------
+// One block joins one cut item: weights 2^(m_i - m) of its parts' sums.  Few
+// parts (long row tiles): a warp a row.  Many parts (a long cache, few rows):
+// the block's warps share the parts of each row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedHeader* __restrict__ hdr, int E, int BR,
+                                                            const float* __restrict__ part_o,
+                                                            const float* __restrict__ part_ml, T* __restrict__ out,
+                                                            float* __restrict__ lse, PagedDims dm) {
+  constexpr int C = D / 32;
+  __shared__ float sm_o[8][D];
+  __shared__ float sm_l[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int w = blockIdx.x; w < E; w += gridDim.x) {
+    const PagedHeader h = hdr[w];
+    if (h.parts == 0) continue;
+    const bool share = h.parts > 8;
+    for (int r = share ? 0 : warp; r < h.rows; r += share ? 1 : 8) {
+      // part 0 is slot 2w + 1, part i > 0 is slot 2(w + i)
+      auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)) * BR + r; };
+      float m = -INFINITY;
+      for (int i = lane; i < h.parts; i += 32) m = fmaxf(m, part_ml[2 * slot(i)]);
+      m = warp_max(m);
+      const float mb = m == -INFINITY ? 0.f : m;
+      float l = 0.f, o[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll 4
+      for (int i = share ? warp : 0; i < h.parts; i += share ? 8 : 1) {
+        const size_t sl = slot(i);
+        const float wt = exp2f(part_ml[2 * sl] - mb);
+        l = fmaf(part_ml[2 * sl + 1], wt, l);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = fmaf(part_o[sl * D + lane * C + c], wt, o[c]);
+      }
+      if (share) {
+        if (lane == 0) sm_l[warp] = l;
+#pragma unroll
+        for (int c = 0; c < C; ++c) sm_o[warp][lane * C + c] = o[c];
+        __syncthreads();
+        if (warp == 0) {
+          l = 0.f;
+#pragma unroll
+          for (int c = 0; c < C; ++c) o[c] = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            l += sm_l[i];
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] += sm_o[i][lane * C + c];
+          }
+        }
+      }
+      if (!share || warp == 0) {
+        const int row = h.row0 + r, tok = row / dm.G, head = h.h * dm.G + row % dm.G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* dst = out + ((size_t)(h.first + tok) * dm.hq + head) * D + lane * C;
+#pragma unroll
+        for (int c = 0; c < C; ++c) dst[c] = from_f32<T>(o[c] * inv);
+        if (lane == 0 && lse != nullptr)
+          lse[(size_t)head * dm.tokens + h.first + tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      if (share) __syncthreads();
+    }
+  }
+}
+
+namespace {
+
+// ---- CUDA-core kernel ----------------------------------------------------------
+// A worker is a warp: R rows of a group, its lanes the channels (D / 32 each),
+// 8 keys at a time straight from the pages into registers, one coalesced row a
+// load.  The 8 R dot products are summed over the lanes by halving: each step
+// sends half of the values, so that 62 shuffles do the work of 320 for R = 8.
+constexpr int kVecThreads = 256, kVecWarps = 8;
+constexpr int kVecBK = 16;                        // keys a tile: the smallest page
+// blocks an SM: 4 rows fit 128 registers a thread, 8 rows do not
+constexpr int vec_blocks(int R) { return R == 4 ? 2 : 1; }
+constexpr int vec_workers(int R) { return 148 * vec_blocks(R) * kVecWarps; }
+constexpr int kVecMinTiles = 4;                   // a worker takes 64 keys at least
+
+template <typename T, int C> struct LaneVec;      // C channels as loaded
+template <> struct LaneVec<float, 4> {
+  float4 v;
+  MOBA_DEV void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  MOBA_DEV void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  MOBA_DEV void widen(float* f) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <> struct LaneVec<float, 2> {
+  float2 v;
+  MOBA_DEV void load(const float* p) { v = __ldg(reinterpret_cast<const float2*>(p)); }
+  MOBA_DEV void zero() { v = make_float2(0.f, 0.f); }
+  MOBA_DEV void widen(float* f) const { f[0] = v.x; f[1] = v.y; }
+};
+template <> struct LaneVec<__nv_bfloat16, 4> {
+  uint2 v;
+  MOBA_DEV void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  MOBA_DEV void zero() { v = make_uint2(0, 0); }
+  MOBA_DEV void widen(float* f) const {
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+template <> struct LaneVec<__nv_bfloat16, 2> {
+  uint32_t v;
+  MOBA_DEV void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  MOBA_DEV void zero() { v = 0; }
+  MOBA_DEV void widen(float* f) const {
+    f[0] = __uint_as_float(v << 16); f[1] = __uint_as_float(v & 0xffff0000u);
+  }
+};
+
+// values v[0 .. N) of every lane summed over the 32 lanes: lane i ends with the
+// sums of values i N / 32 .. (i + 1) N / 32 - 1, in v[0 .. N / 32)
+template <int N>
+MOBA_DEV void halving_sum(float* v, int lane) {
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    n >>= 1;
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (i < n) {
+        const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+  }
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(PagedArgs a, PagedDims dm, PagedHeader* __restrict__ hdr,
+                                                                   float* __restrict__ part_o,
+                                                                   float* __restrict__ part_ml) {
+  constexpr int C = D / 32, N = 8 * R, V = N / 32, LPR = 32 / R;   // values a lane, lanes a row
+  __shared__ PagedPlan<kVecThreads> plan;
+  __shared__ __align__(16) float sp[kVecWarps][N];
+  __shared__ float sa[kVecWarps][R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t W = paged_plan<R, kVecBK, kVecThreads>(plan, a.cu, a.kv_len, dm);
+  const int64_t E = min((int64_t)vec_workers(R), (W + kVecMinTiles - 1) / kVecMinTiles);
+  const int64_t w = (int64_t)blockIdx.x * kVecWarps + warp;
+  if (lane == 0) hdr[w].parts = 0;
+  if (blockIdx.x == 0 && a.status != nullptr)
+    for (int b = threadIdx.x; b < dm.batch; b += kVecThreads)
+      if (a.kv_len[b] > ((int64_t)dm.max_pages << dm.page_shift)) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
+  if (w >= E) return;
+  const T* kp = (const T*)a.k_pool;
+  const T* vp = (const T*)a.v_pool;
+  const int myrow = lane / LPR;
+  int64_t pos = w * W / E;
+  const int64_t stop = (w + 1) * W / E;
+  PagedItem it = paged_locate<R, kVecBK, kVecThreads>(plan, pos, a.cu, a.kv_len, dm);
+
+  while (pos < stop) {
+    const int t0 = it.tile, t1 = (int)min((int64_t)it.tiles, it.tile + (stop - pos));
+    const int row0 = it.rt * R, rows = min(R, it.s.n * dm.G - row0);
+    const int old = it.s.len - it.s.n;
+    float q[R][C], o[R][C];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      LaneVec<T, C> x;
+      x.zero();
+      if (r < rows) {
+        const int tok = (row0 + r) / dm.G, g = (row0 + r) % dm.G;
+        x.load((const T*)a.q + (int64_t)(it.s.first + tok) * dm.q_stride + (it.h * dm.G + g) * D + lane * C);
+      }
+      x.widen(q[r]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        q[r][c] *= dm.scale_log2;
+        o[r][c] = 0.f;
+      }
+    }
+    // keys that the lane's row sees, and that every row of the tile sees
+    const int lim = myrow < rows ? old + (row0 + myrow) / dm.G + 1 : 0;
+    const int all = old + row0 / dm.G + 1;
+    float m = -INFINITY, l = 0.f;
+
+    for (int t = t0; t < t1; ++t) {
+      const int u0 = t * kVecBK;
+      const int pi = u0 >> dm.page_shift;
+      int page = -1;
+      if (u0 < it.s.len) {
+        page = a.table[(int64_t)it.b * dm.max_pages + pi];
+        if (page < 0 || page >= dm.num_pages) {
+          // keys of a page that the pool does not have read as zeros
+          page = -1;
+          if (lane == 0 && a.status != nullptr) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
+        }
+      }
+      const int64_t in_page = ((int64_t)it.h << dm.page_shift) + (u0 & ((1 << dm.page_shift) - 1));
+      const T* kt = kp + page * dm.k_page_stride + in_page * D + lane * C;
+      const T* vt = vp + page * dm.v_page_stride + in_page * D + lane * C;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int u = u0 + 8 * half;
+        if (u >= it.s.len && u > u0) break;
+        LaneVec<T, C> kr[8], vr[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          kr[i].zero();
+          vr[i].zero();
+          if (page >= 0 && u + i < it.s.len) {
+            kr[i].load(kt + (8 * half + i) * D);
+            vr[i].load(vt + (8 * half + i) * D);
+          }
+        }
+        float z[N];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float k[C];
+          kr[i].widen(k);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float d = q[r][0] * k[0];
+#pragma unroll
+            for (int c = 1; c < C; ++c) d = fmaf(q[r][c], k[c], d);
+            z[r * 8 + i] = d;
+          }
+        }
+        halving_sum<N>(z, lane);
+        // the lane's V values: row myrow, keys (lane % LPR) V ..
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (u + (lane % LPR) * V + v >= lim) z[v] = -INFINITY;
+          top = fmaxf(top, z[v]);
+        }
+#pragma unroll
+        for (int x = LPR / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - base);
+        l *= f;
+        m = mn;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float p = exp2f(z[v] - base);
+          l += p;
+          sp[warp][lane * V + v] = p;
+        }
+        const bool moved = __any_sync(0xffffffffu, f != 1.f);
+        if (lane % LPR == 0) sa[warp][myrow] = f;
+        __syncwarp();
+        if (moved) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float fr = sa[warp][r];
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[r][c] *= fr;
+          }
+        }
+        float v[8][C];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vr[i].widen(v[i]);
+        if (u + 8 <= all) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float p[8];
+            *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(&sp[warp][r * 8]);
+            *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(&sp[warp][r * 8 + 4]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int c = 0; c < C; ++c) o[r][c] = fmaf(p[i], v[i][c], o[r][c]);
+          }
+        } else {
+          // some row does not see all of these keys: an infinity or NaN there
+          // must not meet its zero probability
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int lr = r < rows ? old + (row0 + r) / dm.G + 1 : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float p = sp[warp][r * 8 + i];
+              if (u + i < lr) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[r][c] = fmaf(p, v[i][c], o[r][c]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int x = LPR / 2; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+
+    const bool begins = t0 == 0, ends = t1 == it.tiles;
+    const size_t slot = (size_t)(begins ? 2 * w + 1 : 2 * w) * R;
+    if (!(begins && ends) && begins && lane == 0) {
+      PagedHeader h;
+      h.parts = paged_parts(pos + it.tiles, W, E, w);
+      h.first = it.s.first;
+      h.h = it.h;
+      h.row0 = row0;
+      h.rows = rows;
+      h.pad[0] = h.pad[1] = h.pad[2] = 0;
+      hdr[w] = h;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float lr = __shfl_sync(0xffffffffu, l, r * LPR), mr = __shfl_sync(0xffffffffu, m, r * LPR);
+      if (r >= rows) continue;
+      if (begins && ends) {
+        const int tok = it.s.first + (row0 + r) / dm.G, head = it.h * dm.G + (row0 + r) % dm.G;
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+        T* dst = (T*)a.out + ((size_t)tok * dm.hq + head) * D + lane * C;
+#pragma unroll
+        for (int c = 0; c < C; ++c) dst[c] = from_f32<T>(o[r][c] * inv);
+        if (lane == 0 && a.lse != nullptr)
+          a.lse[(size_t)head * dm.tokens + tok] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) part_o[(slot + r) * D + lane * C + c] = o[r][c];
+        if (lane == 0) {
+          part_ml[2 * (slot + r)] = mr;
+          part_ml[2 * (slot + r) + 1] = lr;
+        }
+      }
+    }
+    pos += t1 - t0;
+    if (pos < stop) paged_next<R, kVecBK>(it, a.cu, a.kv_len, dm);
+  }
+}
+
+struct PagedWs {
+  PagedHeader* hdr;
+  float *part_o, *part_ml;
+};
+PagedWs ws_layout(void* ws, int64_t E, int BR, int D) {
+  PagedWs l;
+  char* p = (char*)ws;
+  l.hdr = (PagedHeader*)p;
+  p += E * sizeof(PagedHeader);
+  l.part_ml = (float*)p;
+  p += 2 * E * BR * 2 * sizeof(float);
+  l.part_o = (float*)p;
+  return l;
+}
+size_t ws_bytes(int64_t E, int BR, int D) {
+  return E * sizeof(PagedHeader) + 2 * E * BR * (size_t)(D + 2) * sizeof(float);
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_vec(const PagedDims& dm, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches) {
+  constexpr int kE = vec_workers(R);
+  const PagedWs l = ws_layout(ws, kE, R, D);
+  paged_vec_kernel<T, D, R><<<kE / kVecWarps, kVecThreads, 0, stream>>>(a, dm, l.hdr, l.part_o, l.part_ml);
+  ++*launches;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  paged_combine_kernel<T, D><<<kE / 8, 256, 0, stream>>>(l.hdr, kE, R, l.part_o, l.part_ml, (T*)a.out,
+                                                                a.lse, dm);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_vec_rows(const PagedDims& dm, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches) {
+  if ((int64_t)dm.tokens * dm.G <= 4 * (int64_t)dm.batch) return launch_vec<T, D, 4>(dm, a, ws, stream, launches);
+  return launch_vec<T, D, 8>(dm, a, ws, stream, launches);
+}
+
+}  // namespace
+
+size_t paged_attn_ws(int dtype, int d) {
+  const size_t a = ws_bytes(vec_workers(4), 4, d), b = ws_bytes(vec_workers(8), 8, d);
+  return a > b ? a : b;
+}
+
+cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const PagedArgs& a, void* ws, cudaStream_t stream,
+                              int* launches) {
+  if (dm.tokens == 0) return cudaSuccess;
+  if (dtype == MOBA_BF16)
+    return d == 128 ? launch_vec_rows<__nv_bfloat16, 128>(dm, a, ws, stream, launches)
+                    : launch_vec_rows<__nv_bfloat16, 64>(dm, a, ws, stream, launches);
+  return d == 128 ? launch_vec_rows<float, 128>(dm, a, ws, stream, launches)
+                  : launch_vec_rows<float, 64>(dm, a, ws, stream, launches);
+}
+
+}  // namespace moba
