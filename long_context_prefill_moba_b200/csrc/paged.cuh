@@ -144,6 +144,26 @@ struct PagedHeader {
   int pad[3];
 };
 
+struct PagedWs {
+  PagedHeader* hdr;
+  float *part_o, *part_ml;   // [2 E, BR, D] sums and [2 E, BR] (base, denominator)
+};
+inline PagedWs paged_ws_layout(void* ws, int64_t E, int BR) {
+  PagedWs l;
+  char* p = (char*)ws;
+  l.hdr = (PagedHeader*)p;
+  p += E * sizeof(PagedHeader);
+  l.part_ml = (float*)p;
+  p += 2 * E * BR * 2 * sizeof(float);
+  l.part_o = (float*)p;
+  return l;
+}
+inline size_t paged_ws_bytes(int64_t E, int BR, int D) {
+  return E * sizeof(PagedHeader) + 2 * E * BR * (size_t)(D + 2) * sizeof(float);
+}
+cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int BR, const PagedArgs& a, const PagedDims& dm,
+                                 cudaStream_t stream, int* launches);
+
 // parts of the item that worker w begins at tile `at` of the line and that ends
 // at tile `end`: the workers whose ranges reach into [at, end)
 MOBA_DEV int paged_parts(int64_t end, int64_t W, int64_t E, int64_t w) {

@@ -5,6 +5,8 @@
 //   m = max z, l = sum 2^(z - m), o = sum 2^(z - m) v_u / l, lse = m + log l
 // in one pass over the keys with a running (m, l, o); z in units of log2(e).
 // A row that sees no key gives o = 0, lse = -inf.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace moba {
@@ -334,36 +336,15 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
   }
 }
 
-struct PagedWs {
-  PagedHeader* hdr;
-  float *part_o, *part_ml;
-};
-PagedWs ws_layout(void* ws, int64_t E, int BR, int D) {
-  PagedWs l;
-  char* p = (char*)ws;
-  l.hdr = (PagedHeader*)p;
-  p += E * sizeof(PagedHeader);
-  l.part_ml = (float*)p;
-  p += 2 * E * BR * 2 * sizeof(float);
-  l.part_o = (float*)p;
-  return l;
-}
-size_t ws_bytes(int64_t E, int BR, int D) {
-  return E * sizeof(PagedHeader) + 2 * E * BR * (size_t)(D + 2) * sizeof(float);
-}
-
 template <typename T, int D, int R>
 cudaError_t launch_vec(const PagedDims& dm, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches) {
   constexpr int kE = vec_workers(R);
-  const PagedWs l = ws_layout(ws, kE, R, D);
+  const PagedWs l = paged_ws_layout(ws, kE, R);
   paged_vec_kernel<T, D, R><<<kE / kVecWarps, kVecThreads, 0, stream>>>(a, dm, l.hdr, l.part_o, l.part_ml);
   ++*launches;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_combine_kernel<T, D><<<kE / 8, 256, 0, stream>>>(l.hdr, kE, R, l.part_o, l.part_ml, (T*)a.out,
-                                                                a.lse, dm);
-  ++*launches;
-  return cudaGetLastError();
+  return launch_paged_combine(sizeof(T) == 2 ? MOBA_BF16 : MOBA_F32, D, l, kE, R, a, dm, stream, launches);
 }
 
 template <typename T, int D>
@@ -374,17 +355,44 @@ cudaError_t launch_vec_rows(const PagedDims& dm, const PagedArgs& a, void* ws, c
 
 }  // namespace
 
+cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int BR, const PagedArgs& a, const PagedDims& dm,
+                                 cudaStream_t stream, int* launches) {
+  const int grid = E < 148 ? E : 148;
+  auto go = [&](auto* out, auto dim) {
+    using T = typename std::remove_pointer<decltype(out)>::type;
+    paged_combine_kernel<T, decltype(dim)::value><<<grid, 256, 0, stream>>>(l.hdr, E, BR, l.part_o, l.part_ml, out, a.lse, dm);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == MOBA_BF16) {
+    if (d == 128) go((__nv_bfloat16*)a.out, D128()); else go((__nv_bfloat16*)a.out, D64());
+  } else {
+    if (d == 128) go((float*)a.out, D128()); else go((float*)a.out, D64());
+  }
+  ++*launches;
+  return cudaGetLastError();
+}
+
+size_t paged_tc_ws(int d);
+cudaError_t launch_paged_tc(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
+
 size_t paged_attn_ws(int dtype, int d) {
-  const size_t a = ws_bytes(vec_workers(4), 4, d), b = ws_bytes(vec_workers(8), 8, d);
-  return a > b ? a : b;
+  size_t most = dtype == MOBA_BF16 ? paged_tc_ws(d) : 0;
+  for (int R : {4, 8}) {
+    const size_t b = paged_ws_bytes(vec_workers(R), R, d);
+    most = most > b ? most : b;
+  }
+  return most;
 }
 
 cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const PagedArgs& a, void* ws, cudaStream_t stream,
                               int* launches) {
   if (dm.tokens == 0) return cudaSuccess;
-  if (dtype == MOBA_BF16)
+  if (dtype == MOBA_BF16) {
+    if ((int64_t)dm.tokens * dm.G > 16 * (int64_t)dm.batch) return launch_paged_tc(dm, d, a, ws, stream, launches);
     return d == 128 ? launch_vec_rows<__nv_bfloat16, 128>(dm, a, ws, stream, launches)
                     : launch_vec_rows<__nv_bfloat16, 64>(dm, a, ws, stream, launches);
+  }
   return d == 128 ? launch_vec_rows<float, 128>(dm, a, ws, stream, launches)
                   : launch_vec_rows<float, 64>(dm, a, ws, stream, launches);
 }

@@ -49,10 +49,10 @@ def new_tokens(cu_new, kv_len):
     return got
 
 
-def paged_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale):
+def paged_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale, only=None):
     """out [T, hq, d], lse [hq, T], and the bounds' sums: the largest sum of |q_c k_c|
     of a row's keys and sum_u p_u |v_u|.  Rows of no sequence, and rows that see no
-    key, are 0 and -inf."""
+    key, are 0 and -inf.  `only`: the rows to compute (all)."""
     T, hq, d = q.shape
     hkv, page = k_pool.shape[1:3]
     G = hq // hkv
@@ -67,7 +67,7 @@ def paged_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale):
             k, v = k_pool[at, h // G, slot], v_pool[at, h // G, slot]
             for i in range(n):
                 see = L - n + i + 1
-                if see <= 0:
+                if see <= 0 or (only is not None and first + i not in only):
                     continue
                 z = k[:see] @ q[first + i, h] * scale
                 m = z.max()

@@ -67,22 +67,25 @@ class Cache:
 
 
 def check_attention(c, q, out, lse, scale=None, rows=None):
+    """Every row, or the given ones."""
     d = c.d
     scale = d ** -0.5 if scale is None else scale
     kn, vn = np.nan_to_num(np64(c.k_pool)), np.nan_to_num(np64(c.v_pool))
     want, wlse, dots, absv = O.paged_attention(np64(q)[:c.total], kn, vn, c.cu.numpy(), c.kv_len.numpy(),
-                                               c.table.numpy(), scale)
+                                               c.table.numpy(), scale, rows and set(rows))
     L = max(max(x for _, x in c.lens), 1)
     e = (d + 8) * U * scale * dots + (L + 64) * U
     vmax = np.abs(vn).max() if vn.size else 0.0
     tol = 2 * e[..., None] * vmax + half_step(q.dtype) * np.abs(want)
     if q.dtype != torch.float32:
         tol = tol + 2 * half_step(q.dtype) * absv
+    at = list(range(c.total)) if rows is None else sorted(rows)
     err = np.abs(np64(out)[:c.total] - want)
     assert not np.isnan(np64(out)[:c.total]).any()
-    assert (err <= tol + 1e-30).all(), float(np.max(err / (tol + 1e-30)))
+    assert (err <= tol + 1e-30)[at].all(), float(np.max((err / (tol + 1e-30))[at]))
     if lse is not None:
-        got = np64(lse)[:, :c.total]
+        got = np64(lse)[:, at]
+        wlse, e = wlse[:, at], e[at]
         assert (np.isneginf(got) == np.isneginf(wlse)).all()
         fine = np.isfinite(wlse)
         assert (np.abs(got[fine] - wlse[fine]) <= (e.T + 4 * U)[fine] + 2 * U * np.abs(wlse[fine])).all()
@@ -132,6 +135,30 @@ def test_attention(cuda_device, case):
     assert (out[c.total:] == 7.0).all()          # rows behind the last sequence
     again, lse2 = M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index, return_lse=True)
     assert torch.equal(again[:c.total], out[:c.total]) and torch.equal(lse2[:, :c.total], lse[:, :c.total])
+
+
+@pytest.mark.parametrize("case", [
+    ([(1500, 6000), (0, 30), (700, 700), (1, 5000)], 32, 16, 4, 64, "bf16"),
+    ([(1025, 9000), (64, 20000)], 16, 8, 2, 128, "bf16"),
+    ([(3, 3)] * 200 + [(4000, 4100)] + [(70, 400)] * 30, 128, 6, 2, 128, "bf16"),
+    ([(300, 2000), (200, 300)], 64, 8, 8, 128, "f32"),
+    ([(1, 40000), (1, 90000)], 64, 8, 2, 128, "bf16"),
+    ([(1, 40000), (2, 30000)], 64, 8, 2, 64, "f32")],
+    ids=lambda c: f"{c[5]}-d{c[4]}-{c[2]}x{c[3]}-p{c[1]}-{len(c[0])}seq-{c[0][0]}")
+def test_attention_of_many_tiles(cuda_device, case):
+    """Enough keys that every worker goes through many tiles and several items: rows at every border and random ones."""
+    import long_context_prefill_moba_b200 as M
+    lens, page, hq, hkv, d, dt = case
+    c = Cache(lens, page, hkv, d, dt, cuda_device)
+    q = c.rand(c.rows, hq, d)
+    out, lse = M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index, return_lse=True)
+    again = M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index)
+    assert torch.equal(again, out)
+    r = np.random.RandomState(0)
+    cu = c.cu.numpy()
+    few = cu if len(cu) < 20 else cu[::25]
+    rows = {int(x) for x in list(few) + [x - 1 for x in few] + list(r.randint(0, c.total, 25)) if 0 <= x < c.total}
+    check_attention(c, q, out, lse, rows=rows)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
