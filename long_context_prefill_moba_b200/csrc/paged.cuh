@@ -11,6 +11,8 @@
 // the combine kernel joins; the others are written by their worker.
 #pragma once
 
+#include <cuda.h>
+
 #include "launch.h"
 
 namespace moba {
@@ -163,6 +165,9 @@ inline size_t paged_ws_bytes(int64_t E, int BR, int D) {
 }
 cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int BR, const PagedArgs& a, const PagedDims& dm,
                                  cudaStream_t stream, int* launches);
+
+// 4-D tensor map of a bf16 pool, [pages][heads][slots][D], boxes of `box` slots x 64 channels, 128-byte swizzle
+bool make_pool_map(CUtensorMap* map, const void* pool, const PagedDims& dm, int D, int64_t page_stride, int box);
 
 // parts of the item that worker w begins at tile `at` of the line and that ends
 // at tile `end`: the workers whose ranges reach into [at, end)

@@ -1,5 +1,6 @@
-// Attention of new tokens over a paged cache, on CUDA cores, and the combine
-// kernel that joins the parts of an item (paged.cuh).
+// Attention of new tokens over a paged cache: the choice of the kernel, the fp32
+// kernel on CUDA cores, and the combine kernel that joins the parts of an item
+// (paged.cuh).
 //
 // For a row at position p with keys u <= p:  z_u = scale <q, k_u>,
 //   m = max z, l = sum 2^(z - m), o = sum 2^(z - m) v_u / l, lse = m + log l
@@ -24,6 +25,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedHeader* _
   __shared__ float sm_o[8][D];
   __shared__ float sm_l[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // launched while the attention kernel runs: what follows waits for its writes
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   for (int w = blockIdx.x; w < E; w += gridDim.x) {
     const PagedHeader h = hdr[w];
     if (h.parts == 0) continue;
@@ -103,24 +106,6 @@ template <> struct LaneVec<float, 2> {
   MOBA_DEV void zero() { v = make_float2(0.f, 0.f); }
   MOBA_DEV void widen(float* f) const { f[0] = v.x; f[1] = v.y; }
 };
-template <> struct LaneVec<__nv_bfloat16, 4> {
-  uint2 v;
-  MOBA_DEV void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
-  MOBA_DEV void zero() { v = make_uint2(0, 0); }
-  MOBA_DEV void widen(float* f) const {
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-};
-template <> struct LaneVec<__nv_bfloat16, 2> {
-  uint32_t v;
-  MOBA_DEV void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint32_t*>(p)); }
-  MOBA_DEV void zero() { v = 0; }
-  MOBA_DEV void widen(float* f) const {
-    f[0] = __uint_as_float(v << 16); f[1] = __uint_as_float(v & 0xffff0000u);
-  }
-};
-
 // values v[0 .. N) of every lane summed over the 32 lanes: lane i ends with the
 // sums of values i N / 32 .. (i + 1) N / 32 - 1, in v[0 .. N / 32)
 template <int N>
@@ -149,6 +134,7 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
   __shared__ __align__(16) float sp[kVecWarps][N];
   __shared__ float sa[kVecWarps][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::);
   const int64_t W = paged_plan<R, kVecBK, kVecThreads>(plan, a.cu, a.kv_len, dm);
   const int64_t E = min((int64_t)vec_workers(R), (W + kVecMinTiles - 1) / kVecMinTiles);
   const int64_t w = (int64_t)blockIdx.x * kVecWarps + warp;
@@ -360,24 +346,41 @@ cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int 
   const int grid = E < 148 ? E : 148;
   auto go = [&](auto* out, auto dim) {
     using T = typename std::remove_pointer<decltype(out)>::type;
-    paged_combine_kernel<T, decltype(dim)::value><<<grid, 256, 0, stream>>>(l.hdr, E, BR, l.part_o, l.part_ml, out, a.lse, dm);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(256);
+    c.stream = stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, paged_combine_kernel<T, decltype(dim)::value>, (const PagedHeader*)l.hdr, E, BR,
+                              (const float*)l.part_o, (const float*)l.part_ml, out, a.lse, dm);
   };
+  cudaError_t e;
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
   if (dtype == MOBA_BF16) {
-    if (d == 128) go((__nv_bfloat16*)a.out, D128()); else go((__nv_bfloat16*)a.out, D64());
+    e = d == 128 ? go((__nv_bfloat16*)a.out, D128()) : go((__nv_bfloat16*)a.out, D64());
   } else {
-    if (d == 128) go((float*)a.out, D128()); else go((float*)a.out, D64());
+    e = d == 128 ? go((float*)a.out, D128()) : go((float*)a.out, D64());
   }
-  ++*launches;
-  return cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
+size_t paged_decode_ws(int d);
+cudaError_t launch_paged_decode(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
 size_t paged_tc_ws(int d);
 cudaError_t launch_paged_tc(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
 
 size_t paged_attn_ws(int dtype, int d) {
-  size_t most = dtype == MOBA_BF16 ? paged_tc_ws(d) : 0;
+  if (dtype == MOBA_BF16) {
+    const size_t a = paged_tc_ws(d), b = paged_decode_ws(d);
+    return a > b ? a : b;
+  }
+  size_t most = 0;
   for (int R : {4, 8}) {
     const size_t b = paged_ws_bytes(vec_workers(R), R, d);
     most = most > b ? most : b;
@@ -390,8 +393,7 @@ cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const Paged
   if (dm.tokens == 0) return cudaSuccess;
   if (dtype == MOBA_BF16) {
     if ((int64_t)dm.tokens * dm.G > 16 * (int64_t)dm.batch) return launch_paged_tc(dm, d, a, ws, stream, launches);
-    return d == 128 ? launch_vec_rows<__nv_bfloat16, 128>(dm, a, ws, stream, launches)
-                    : launch_vec_rows<__nv_bfloat16, 64>(dm, a, ws, stream, launches);
+    return launch_paged_decode(dm, d, a, ws, stream, launches);
   }
   return d == 128 ? launch_vec_rows<float, 128>(dm, a, ws, stream, launches)
                   : launch_vec_rows<float, 64>(dm, a, ws, stream, launches);

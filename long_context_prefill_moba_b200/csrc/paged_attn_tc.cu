@@ -137,6 +137,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   __shared__ PagedPlan<kThreads> plan;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::);
   const int64_t W = paged_plan<kBR, kBK, kThreads>(plan, a.cu, a.kv_len, dm);
   const int64_t E = min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles);
   const int64_t me = blockIdx.x;
@@ -348,6 +349,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const int u = (p.fix0 + (i >> 2)) * kBK + (i & 3) * 32 + __ffs(bits) - 1;
                 if (!valid || u >= lim) continue;
                 const int64_t page = a.table[(int64_t)p.it.b * dm.max_pages + (u >> dm.page_shift)];
+                if (page < 0 || page >= dm.num_pages) continue;
                 const __nv_bfloat16* v = (const __nv_bfloat16*)a.v_pool + page * dm.v_page_stride +
                                          (((int64_t)p.it.h << dm.page_shift) + (u & ((1 << dm.page_shift) - 1))) * D + cc * 32;
 #pragma unroll
@@ -640,20 +642,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (tid == 0 && ctl.abort && a.status != nullptr) atomicExch(a.status, (int)MOBA_ERR_TIMEOUT);
 }
 
-// map of a pool: [pages][heads][slots][D], boxes of `box` slots x 64 channels
-bool make_pool_map(CUtensorMap* map, const void* pool, const PagedDims& dm, int D, int64_t page_stride, int box) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t page = 1ull << dm.page_shift;
-  cuuint64_t dims[4] = {(cuuint64_t)D, page, (cuuint64_t)dm.hkv, (cuuint64_t)dm.num_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, page * D * 2, (cuuint64_t)page_stride * 2};
-  cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, boxes, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cudaStream_t stream) {
   const int box = (1 << dm.page_shift) < kBK ? 1 << dm.page_shift : kBK;
@@ -677,6 +665,20 @@ cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cu
 }
 
 }  // namespace
+
+// map of a pool: [pages][heads][slots][D], boxes of `box` slots x 64 channels
+bool make_pool_map(CUtensorMap* map, const void* pool, const PagedDims& dm, int D, int64_t page_stride, int box) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t page = 1ull << dm.page_shift;
+  cuuint64_t dims[4] = {(cuuint64_t)D, page, (cuuint64_t)dm.hkv, (cuuint64_t)dm.num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, page * D * 2, (cuuint64_t)page_stride * 2};
+  cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, boxes, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 size_t paged_tc_ws(int d) { return paged_ws_bytes(kWorkers, kBR, d); }
 
