@@ -18,32 +18,54 @@
 // cosines once, in shared memory, for all of the token's heads.
 // Sums are fp32; results are rounded once, on the store.
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace moba {
 
 namespace {
 
+using sm100::f2_add;
+using sm100::f2_fma;
+using sm100::f2_pack;
+using sm100::f2_sub;
+using sm100::f2_unpack;
+MOBA_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+MOBA_DEV float f2_sum(uint64_t a) {
+  float x, y;
+  f2_unpack(a, x, y);
+  return x + y;
+}
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSms = 148;
 
-// 8 consecutive elements as loaded
+// 8 consecutive elements as loaded; widened to 4 packed fp32 pairs (the arithmetic
+// below runs on pairs: half the instructions, which bound these kernels before the
+// memory did)
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> {
   uint4 u;
   MOBA_DEV void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   MOBA_DEV void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
   MOBA_DEV void zero() { u = make_uint4(0, 0, 0, 0); }
-  MOBA_DEV void widen(float* f) const {
+  MOBA_DEV void widen(uint64_t* f) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  MOBA_DEV void round(const float* f) {
-    u = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                   pack_bf16x2(f[6], f[7]));
+  MOBA_DEV void round(const uint64_t* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      f2_unpack(f[i], x, y);
+      w[i] = pack_bf16x2(x, y);
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <> struct Raw8<float> {
@@ -57,13 +79,13 @@ template <> struct Raw8<float> {
     *reinterpret_cast<float4*>(p + 4) = b;
   }
   MOBA_DEV void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  MOBA_DEV void widen(float* f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  MOBA_DEV void widen(uint64_t* f) const {
+    f[0] = f2_pack(a.x, a.y); f[1] = f2_pack(a.z, a.w);
+    f[2] = f2_pack(b.x, b.y); f[3] = f2_pack(b.z, b.w);
   }
-  MOBA_DEV void round(const float* f) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  MOBA_DEV void round(const uint64_t* f) {
+    f2_unpack(f[0], a.x, a.y); f2_unpack(f[1], a.z, a.w);
+    f2_unpack(f[2], b.x, b.y); f2_unpack(f[3], b.z, b.w);
   }
 };
 
@@ -83,34 +105,69 @@ MOBA_DEV void lane_vectors(int j, int rot, bool interleaved, int& va, int& vb) {
   }
 }
 
-// cos and sin of the warp's token into cs[rot/2]
-MOBA_DEV void warp_angles(float2* cs, int pos, const double* __restrict__ inv_freq, int half, int lane) {
+// cos and sin of the warp's token, for pair 8 j + e of lane j at
+// [e / 4][cos, sin][j][e % 4]: a lane's reads are 16 bytes, without bank conflicts
+// (as (cos, sin) pair after pair they took 70% of the shared memory's time)
+template <int LPH> struct Angles { float4 v[2][2][LPH]; };
+template <int LPH>
+MOBA_DEV void warp_angles(Angles<LPH>& cs, int pos, const double (&freq)[LPH / 4], int half, int lane) {
   constexpr double kInv2Pi = 0.15915494309189533576888;
-  for (int i = lane; i < half; i += 32) {
-    double turns = (double)pos * inv_freq[i] * kInv2Pi;
+  float* f = reinterpret_cast<float*>(&cs);
+  __syncwarp();   // the last token's angles are read
+#pragma unroll
+  for (int n = 0; n < LPH / 4; ++n) {
+    const int i = lane + 32 * n;
+    if (i >= half) continue;
+    double turns = (double)pos * freq[n] * kInv2Pi;
     turns -= rint(turns);
     float s, c;
     sincospif((float)(2.0 * turns), &s, &c);
-    cs[i] = make_float2(c, s);
+    const int at = ((((i >> 2) & 1) * 2 * LPH + (i >> 3)) << 2) + (i & 3);
+    f[at] = c;
+    f[at + 4 * LPH] = s;
   }
   __syncwarp();
 }
 
-// rotate the lane's 16 elements y = (a[8], b[8]) by its 8 pairs' angles (way =
-// 1), or back (way = -1)
-MOBA_DEV void turn(float* y, const float2* cs, bool interleaved, float way) {
+// turn the lane's 8 packed pairs of elements (vectors a = y[0..4), b = y[4..8))
+// by its angles, or back
+template <int LPH, bool kBack>
+MOBA_DEV void turn(uint64_t* y, const Angles<LPH>& cs, int j, bool interleaved) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 t = cs[e];
-    const float s = way * t.y;
-    const int ia = interleaved ? 2 * e : e, ib = interleaved ? 2 * e + 1 : 8 + e;
-    const float a = y[ia], b = y[ib];
-    y[ia] = a * t.x - b * s;
-    y[ib] = b * t.x + a * s;
+  for (int h = 0; h < 2; ++h) {
+    const float4 c = cs.v[h][0][j], s = cs.v[h][1][j];
+    if (interleaved) {
+      // (a, b) of pair 4 h + i is the packed y[4 h + i]
+      const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_unpack(y[4 * h + i], a, b);
+        const float t = kBack ? -sv[i] : sv[i];
+        y[4 * h + i] = f2_pack(a * cv[i] - b * t, b * cv[i] + a * t);
+      }
+    } else {
+      const uint64_t c2[2] = {f2_pack(c.x, c.y), f2_pack(c.z, c.w)}, s2[2] = {f2_pack(s.x, s.y), f2_pack(s.z, s.w)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t a = y[2 * h + i], b = y[4 + 2 * h + i];
+        if (kBack) {
+          y[2 * h + i] = f2_fma(b, s2[i], f2_mul(a, c2[i]));
+          y[4 + 2 * h + i] = f2_sub(f2_mul(b, c2[i]), f2_mul(a, s2[i]));
+        } else {
+          y[2 * h + i] = f2_sub(f2_mul(a, c2[i]), f2_mul(b, s2[i]));
+          y[4 + 2 * h + i] = f2_fma(a, s2[i], f2_mul(b, c2[i]));
+        }
+      }
+    }
   }
 }
-MOBA_DEV void turn_lane(float* y, const float2* cs, bool interleaved, float way) {
-  if (interleaved) turn(y, cs, true, way); else turn(y, cs, false, way);
+
+// the lane's frequencies: of pairs lane and lane + 32
+template <int N>
+MOBA_DEV void load_freq(double (&f)[N], const double* __restrict__ inv_freq, int half, int lane) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) f[n] = lane + 32 * n < half ? inv_freq[lane + 32 * n] : 0.0;
 }
 
 template <int LPH>
@@ -120,17 +177,16 @@ MOBA_DEV float head_sum(float v) {
   return v;
 }
 
-// 16 weights of the lane's two vectors, in fp32
-template <typename T>
-MOBA_DEV void load_weights(float* w, const void* p, int wf32, int va, int vb) {
+// 16 weights of the lane's two vectors, in packed fp32
+MOBA_DEV void load_weights(uint64_t* w, const void* p, int wf32, int va, int vb) {
   if (wf32) {
     Raw8<float> r;
     r.load((const float*)p + 8 * va); r.widen(w);
-    r.load((const float*)p + 8 * vb); r.widen(w + 8);
+    r.load((const float*)p + 8 * vb); r.widen(w + 4);
   } else {
     Raw8<__nv_bfloat16> r;
     r.load((const __nv_bfloat16*)p + 8 * va); r.widen(w);
-    r.load((const __nv_bfloat16*)p + 8 * vb); r.widen(w + 8);
+    r.load((const __nv_bfloat16*)p + 8 * vb); r.widen(w + 4);
   }
 }
 
@@ -148,16 +204,24 @@ MOBA_DEV int seq_of_token(const int32_t* __restrict__ cu, int batch, int t, int 
   return min(lo + c, batch - 1);
 }
 
-// One warp = one token (or every split-th head group of it, where there are
-// few tokens).
+// Head groups loaded ahead of the one in work: 2 of bf16 (1 KB each), 1 of fp32.
+// At one, warps waited for their loads 60% of the time.
+template <typename T> constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
+template <typename T> constexpr int kFwdBlocks = sizeof(T) == 2 ? 3 : 2;   // an SM, for 80 and 128 registers
+
+// A warp takes tokens in a stride (or every split-th head group of them, where
+// there are few tokens) as one run of head groups, loads running ahead across
+// tokens.
 template <typename T, int D, bool kAppend>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(RopeArgs a) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH;
-  __shared__ float2 cs_all[kWarps][D / 2];
+__global__ void __launch_bounds__(kThreads, kFwdBlocks<T>) norm_rope_kernel(RopeArgs a) {
+  constexpr int LPH = D / 16, HPW = 32 / LPH, kRing = kAhead<T> + 1;
+  __shared__ Angles<LPH> cs_all[kWarps];
+  __shared__ ulonglong2 sm_w[2][4][LPH];   // weights of queries and keys as lane j reads them
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
-  const int t = (int)(gw / a.split), s = (int)(gw % a.split);
-  if (t >= a.tokens) return;
+  const int gw = blockIdx.x * kWarps + warp;
+  const int s = gw % a.split, t0 = gw / a.split, step = gridDim.x * kWarps / a.split;
+  // rows behind the last sequence are left as they were
+  const int tokens = kAppend ? min(a.tokens, a.cu[a.batch]) : a.tokens;
   const int j = lane % LPH, hl = lane / LPH;
   int va, vb;
   lane_vectors<D>(j, a.rot, a.interleaved != 0, va, vb);
@@ -169,98 +233,137 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(RopeArgs a) {
     head = (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * HPW + hl;
     return head < (kind == 0 ? a.hq : a.hkv);
   };
-  auto load = [&](int g, Raw8<T>& x0, Raw8<T>& x1) {
+  int lt = t0, lg = s;   // the next group to load
+  Raw8<T> ring[kRing][2];
+  auto load = [&](Raw8<T> (&x)[2]) {
     int kind, head;
-    x0.zero();
-    x1.zero();
-    if (g >= groups || !locate(g, kind, head)) return;
-    const T* p = kind == 0 ? (const T*)a.q + t * a.q_stride
-                           : kind == 1 ? (const T*)a.k + t * a.k_stride : (const T*)a.v + t * a.v_stride;
-    x0.load(p + head * D + 8 * va);
-    x1.load(p + head * D + 8 * vb);
+    x[0].zero();
+    x[1].zero();
+    if (lt < tokens && locate(lg, kind, head)) {
+      const T* p = kind == 0 ? (const T*)a.q + lt * a.q_stride
+                             : kind == 1 ? (const T*)a.k + lt * a.k_stride : (const T*)a.v + lt * a.v_stride;
+      x[0].load(p + head * D + 8 * va);
+      x[1].load(p + head * D + 8 * vb);
+    }
+    lg += a.split;
+    if (lg >= groups) {
+      lg = s;
+      lt = step < tokens - lt ? lt + step : tokens;
+    }
   };
-  Raw8<T> x0, x1;
-  load(s, x0, x1);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load(ring[i]);
 
-  int pos, slot = 0;
-  int64_t page = -1;
-  if (kAppend) {
-    // a row behind the last sequence is left as it was
-    if (t >= a.cu[a.batch]) return;
-    const int b = seq_of_token(a.cu, a.batch, t, lane);
-    pos = a.kv_len[b] - (a.cu[b + 1] - t);
-    const int pi = pos >> a.page_shift;
-    slot = pos & ((1 << a.page_shift) - 1);
-    if (pos >= 0 && pi < a.max_pages) page = a.table[(int64_t)b * a.max_pages + pi];
-    if (page < 0 || page >= a.num_pages) {
-      // no page for this token: nothing is written, the status word says so
-      page = -1;
-      if (lane == 0 && a.status != nullptr) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
+  if (warp < 2 && lane < LPH) {
+    const void* wp = warp == 0 ? a.q_weight : a.k_weight;
+    if (wp != nullptr) {
+      uint64_t w[8];
+      load_weights(w, wp, a.weight_f32, va, vb);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sm_w[warp][e][j] = make_ulonglong2(w[2 * e], w[2 * e + 1]);
     }
-  } else {
-    pos = a.positions != nullptr ? a.positions[t] : 0;
   }
+  __syncthreads();
+  if (t0 >= tokens) return;
+  double freq[LPH / 4];
+  load_freq(freq, a.inv_freq, a.rot / 2, lane);
   const bool rotated = j < a.rot / 16;
-  const float2* cs = cs_all[warp] + 8 * j;
-  if (a.rot > 0) warp_angles(cs_all[warp], pos, a.inv_freq, a.rot / 2, lane);
-
-  float w[16];
-  int have = -1;
-  for (int g = s; g < groups; g += a.split) {
-    Raw8<T> n0, n1;
-    load(g + a.split, n0, n1);
-    int kind, head;
-    const bool live = locate(g, kind, head);
-    T* dst;
-    if (kind == 0) {
-      dst = (T*)a.q_out + ((int64_t)t * a.hq + head) * D;
-    } else if (!kAppend) {
-      dst = (T*)a.k_out + ((int64_t)t * a.hkv + head) * D;
-    } else {
-      dst = (kind == 1 ? (T*)a.k_out + page * a.k_page_stride : (T*)a.v_out + page * a.v_page_stride) +
-            (((int64_t)head << a.page_shift) + slot) * D;
-    }
-    const bool put = live && (kind == 0 || !kAppend || page >= 0);
-    if (!kAppend || kind < 2) {
-      const void* wp = kind == 0 ? a.q_weight : a.k_weight;
-      float y[16];
-      x0.widen(y);
-      x1.widen(y + 8);
-      if (wp != nullptr) {
-        if (have != kind) {
-          load_weights<T>(w, wp, a.weight_f32, va, vb);
-          have = kind;
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(y[e], y[e], ss);
-        const float r = rsqrtf(head_sum<LPH>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] *= r * w[e];
+  const Angles<LPH>& cs = cs_all[warp];
+  int slot = 0;
+  int64_t page = -1;
+  int next_pos = !kAppend && a.rot > 0 ? a.positions[t0] : 0;
+  // position, page and angles of a token
+  auto begin = [&](int t) {
+    int pos;
+    if (kAppend) {
+      const int b = seq_of_token(a.cu, a.batch, t, lane);
+      pos = a.kv_len[b] - (a.cu[b + 1] - t);
+      const int pi = pos >> a.page_shift;
+      slot = pos & ((1 << a.page_shift) - 1);
+      page = -1;
+      if (pos >= 0 && pi < a.max_pages) page = a.table[(int64_t)b * a.max_pages + pi];
+      if (page < 0 || page >= a.num_pages) {
+        // no page for this token: nothing is written, the status word says so
+        page = -1;
+        if (lane == 0 && a.status != nullptr) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
       }
-      if (rotated) turn_lane(y, cs, a.interleaved != 0, 1.f);
-      x0.round(y);
-      x1.round(y + 8);
+    } else {
+      pos = next_pos;
+      if (a.rot > 0 && step < tokens - t) next_pos = a.positions[t + step];
     }
-    if (put) {
-      x0.store(dst + 8 * va);
-      x1.store(dst + 8 * vb);
+    if (a.rot > 0) warp_angles<LPH>(cs_all[warp], pos, freq, a.rot / 2, lane);
+  };
+
+  int t = t0, g = s;
+  while (t < tokens) {
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) {
+      if (t >= tokens) break;
+      load(ring[(i + kRing - 1) % kRing]);
+      Raw8<T>&x0 = ring[i][0], &x1 = ring[i][1];
+      if (g == s) begin(t);
+      int kind, head;
+      const bool live = locate(g, kind, head);
+      T* dst;
+      if (kind == 0) {
+        dst = (T*)a.q_out + ((int64_t)t * a.hq + head) * D;
+      } else if (!kAppend) {
+        dst = (T*)a.k_out + ((int64_t)t * a.hkv + head) * D;
+      } else {
+        dst = (kind == 1 ? (T*)a.k_out + page * a.k_page_stride : (T*)a.v_out + page * a.v_page_stride) +
+              (((int64_t)head << a.page_shift) + slot) * D;
+      }
+      const bool put = live && (kind == 0 || !kAppend || page >= 0);
+      if (!kAppend || kind < 2) {
+        uint64_t y[8];
+        x0.widen(y);
+        x1.widen(y + 4);
+        if ((kind == 0 ? a.q_weight : a.k_weight) != nullptr) {
+          uint64_t s0 = f2_mul(y[0], y[0]), s1 = f2_mul(y[1], y[1]);
+#pragma unroll
+          for (int e = 2; e < 8; e += 2) {
+            s0 = f2_fma(y[e], y[e], s0);
+            s1 = f2_fma(y[e + 1], y[e + 1], s1);
+          }
+          const float r = rsqrtf(head_sum<LPH>(f2_sum(f2_add(s0, s1))) * (1.f / D) + a.eps);
+          const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const ulonglong2 w = sm_w[kind][e][j];
+            y[2 * e] = f2_mul(y[2 * e], f2_mul(r2, w.x));
+            y[2 * e + 1] = f2_mul(y[2 * e + 1], f2_mul(r2, w.y));
+          }
+        }
+        if (rotated) turn<LPH, false>(y, cs, j, a.interleaved != 0);
+        x0.round(y);
+        x1.round(y + 4);
+      }
+      if (put) {
+        x0.store(dst + 8 * va);
+        x1.store(dst + 8 * vb);
+      }
+      g += a.split;
+      if (g >= groups) {
+        g = s;
+        t = step < tokens - t ? t + step : tokens;
+      }
     }
-    x0 = n0;
-    x1 = n1;
   }
 }
+
+template <typename T> constexpr int kBwdPerSm = sizeof(T) == 2 ? 2 : 1;   // blocks an SM, for 128 and 255 registers
 
 // Backward.  Blocks [0, nbq) take the queries, the rest the keys, so that a
 // lane has one weight gradient (16 channels) to sum; a block's sums go to its
 // row of `part`, in a fixed order, and the reduction kernel adds the rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(RopeArgs a, const void* dq_out, const void* dk_out,
+__global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(RopeArgs a, const void* dq_out, const void* dk_out,
                                                                  float* part, int nbq) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
-  __shared__ float2 cs_all[kWarps][D / 2];
+  __shared__ Angles<LPH> cs_all[kWarps];
   __shared__ float sums[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::);
   const bool isq = (int)blockIdx.x < nbq;
   const int nb = isq ? nbq : gridDim.x - nbq, bi = isq ? blockIdx.x : blockIdx.x - nbq;
   const int heads = isq ? a.hq : a.hkv, groups = (heads + HPW - 1) / HPW;
@@ -272,71 +375,95 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(RopeArgs a, con
   int va, vb;
   lane_vectors<D>(j, a.rot, a.interleaved != 0, va, vb);
   const bool rotated = j < a.rot / 16;
-  const float2* cs = cs_all[warp] + 8 * j;
-  float w[16], dw[16];
-  load_weights<T>(w, isq ? a.q_weight : a.k_weight, a.weight_f32, va, vb);
+  const Angles<LPH>& cs = cs_all[warp];
+  uint64_t w[8], dw[8];
+  load_weights(w, isq ? a.q_weight : a.k_weight, a.weight_f32, va, vb);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
+  for (int e = 0; e < 8; ++e) dw[e] = 0;
 
-  for (int t = bi * kWarps + warp; t < a.tokens; t += nb * kWarps) {
-    Raw8<T> x0, x1, d0, d1;
-    auto load = [&](int g, Raw8<T>& p0, Raw8<T>& p1, Raw8<T>& r0, Raw8<T>& r1) {
-      const int head = g * HPW + hl;
-      if (head < heads) {
-        const T* p = x + t * xs + head * D;
-        const T* r = dy + ((int64_t)t * heads + head) * D;
-        p0.load(p + 8 * va); p1.load(p + 8 * vb);
-        r0.load(r + 8 * va); r1.load(r + 8 * vb);
-      } else {
-        p0.zero(); p1.zero(); r0.zero(); r1.zero();
-      }
-    };
-    load(0, x0, x1, d0, d1);
-    __syncwarp();
-    if (a.rot > 0) warp_angles(cs_all[warp], a.positions[t], a.inv_freq, a.rot / 2, lane);
-    for (int g = 0; g < groups; ++g) {
-      Raw8<T> n0, n1, m0, m1;
-      load(g + 1, n0, n1, m0, m1);
-      float xv[16], z[16];
-      x0.widen(xv); x1.widen(xv + 8);
-      d0.widen(z); d1.widen(z + 8);
-      if (rotated) turn_lane(z, cs, a.interleaved != 0, -1.f);
-      float ss = 0.f, dot = 0.f;
+  double freq[LPH / 4];
+  load_freq(freq, a.inv_freq, a.rot / 2, lane);
+  const int step = nb * kWarps;
+  int lt = bi * kWarps + warp, lg = 0;   // the next group to load: one ahead, across tokens
+  int t = lt, g = 0;
+  auto load = [&](Raw8<T>& p0, Raw8<T>& p1, Raw8<T>& r0, Raw8<T>& r1) {
+    const int head = lg * HPW + hl;
+    if (lt < a.tokens && head < heads) {
+      const T* p = x + lt * xs + head * D;
+      const T* r = dy + ((int64_t)lt * heads + head) * D;
+      p0.load(p + 8 * va); p1.load(p + 8 * vb);
+      r0.load(r + 8 * va); r1.load(r + 8 * vb);
+    } else {
+      p0.zero(); p1.zero(); r0.zero(); r1.zero();
+    }
+    if (++lg >= groups) {
+      lg = 0;
+      lt = lt < a.tokens && step < a.tokens - lt ? lt + step : a.tokens;
+    }
+  };
+  // registers of a group in work and of the next in turn: a copy between them would wait for the loads
+  Raw8<T> ring[2][4];
+  load(ring[0][0], ring[0][1], ring[0][2], ring[0][3]);
+  int next_pos = t < a.tokens && a.rot > 0 ? a.positions[t] : 0;
+  while (t < a.tokens) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        ss = fmaf(xv[e], xv[e], ss);
-        dot = fmaf(xv[e], z[e] * w[e], dot);
+    for (int i = 0; i < 2; ++i) {
+      if (t >= a.tokens) break;
+      load(ring[1 - i][0], ring[1 - i][1], ring[1 - i][2], ring[1 - i][3]);
+      Raw8<T>&x0 = ring[i][0], &x1 = ring[i][1], &d0 = ring[i][2], &d1 = ring[i][3];
+      if (g == 0 && a.rot > 0) {
+        const int pos = next_pos;
+        if (step < a.tokens - t) next_pos = a.positions[t + step];
+        warp_angles<LPH>(cs_all[warp], pos, freq, a.rot / 2, lane);
       }
-      ss = head_sum<LPH>(ss);
-      dot = head_sum<LPH>(dot);
+      uint64_t xv[8], z[8];
+      x0.widen(xv); x1.widen(xv + 4);
+      d0.widen(z); d1.widen(z + 4);
+      if (rotated) turn<LPH, true>(z, cs, j, a.interleaved != 0);
+      uint64_t s0 = 0, s1 = 0, u0 = 0, u1 = 0;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        s0 = f2_fma(xv[e], xv[e], s0);
+        s1 = f2_fma(xv[e + 1], xv[e + 1], s1);
+        u0 = f2_fma(xv[e], f2_mul(z[e], w[e]), u0);
+        u1 = f2_fma(xv[e + 1], f2_mul(z[e + 1], w[e + 1]), u1);
+      }
+      const float ss = head_sum<LPH>(f2_sum(f2_add(s0, s1))), dot = head_sum<LPH>(f2_sum(f2_add(u0, u1)));
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float c = r * r * r * dot * (1.f / D);
+      const float c = -(r * r * r * dot * (1.f / D));
+      const uint64_t r2 = f2_pack(r, r), c2 = f2_pack(c, c);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float rz = r * z[e];
-        dw[e] = fmaf(rz, xv[e], dw[e]);
-        z[e] = rz * w[e] - c * xv[e];
+      for (int e = 0; e < 8; ++e) {
+        const uint64_t rz = f2_mul(r2, z[e]);
+        dw[e] = f2_fma(rz, xv[e], dw[e]);
+        z[e] = f2_fma(c2, xv[e], f2_mul(rz, w[e]));
       }
       const int head = g * HPW + hl;
       if (head < heads) {
         T* p = dx + ((int64_t)t * heads + head) * D;
-        d0.round(z); d1.round(z + 8);
+        d0.round(z); d1.round(z + 4);
         d0.store(p + 8 * va); d1.store(p + 8 * vb);
       }
-      x0 = n0; x1 = n1; d0 = m0; d1 = m1;
+      if (++g >= groups) {
+        g = 0;
+        t = step < a.tokens - t ? t + step : a.tokens;
+      }
     }
   }
   // heads of the warp, then the warps, in order
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 8; ++e) {
+    float x, y;
+    f2_unpack(dw[e], x, y);
 #pragma unroll
-    for (int o = LPH; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-  }
-  if (hl == 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      sums[warp][8 * va + e] = dw[e];
-      sums[warp][8 * vb + e] = dw[8 + e];
+    for (int o = LPH; o < 32; o <<= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if (hl == 0) {
+      const int at = 8 * (e < 4 ? va : vb) + 2 * (e & 3);
+      sums[warp][at] = x;
+      sums[warp][at + 1] = y;
     }
   }
   __syncthreads();
@@ -348,25 +475,26 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(RopeArgs a, con
   }
 }
 
-// dw of the queries (block 0) and of the keys (block 1): the blocks' rows of
-// `part` added by 1024 / D threads a channel, in a fixed order
+// dw of the queries (blocks y = 0) and of the keys (y = 1): 32 channels a block,
+// whose 32 warps add the rows of `part`, in a fixed order.  (One block for all
+// channels took 10 us for 592 rows.)
 template <int D>
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int nbq, int nbk,
                                                             void* dqw, void* dkw, int weight_f32) {
-  constexpr int kParts = 1024 / D;
-  __shared__ float sums[kParts][D];
-  const int c = threadIdx.x % D, p = threadIdx.x / D;
-  const int lo = blockIdx.x == 0 ? 0 : nbq, hi = blockIdx.x == 0 ? nbq : nbq + nbk;
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, p = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // launched while the backward kernel runs
+  const int lo = blockIdx.y == 0 ? 0 : nbq, hi = blockIdx.y == 0 ? nbq : nbq + nbk;
   float v = 0.f;
 #pragma unroll 8
-  for (int i = lo + p; i < hi; i += kParts) v += part[(int64_t)i * D + c];
-  sums[p][c] = v;
+  for (int i = lo + p; i < hi; i += 32) v += part[(int64_t)i * D + c];
+  sums[p][lane] = v;
   __syncthreads();
-  if (p == 0) {
-#pragma unroll
-    for (int i = 1; i < kParts; ++i) v += sums[i][c];
-    void* dst = blockIdx.x == 0 ? dqw : dkw;
-    if (weight_f32) ((float*)dst)[c] = v; else ((__nv_bfloat16*)dst)[c] = __float2bfloat16_rn(v);
+  v = warp_sum(sums[lane][p]);   // channel p of the block
+  if (lane == 0) {
+    void* dst = blockIdx.y == 0 ? dqw : dkw;
+    const int at = blockIdx.x * 32 + p;
+    if (weight_f32) ((float*)dst)[at] = v; else ((__nv_bfloat16*)dst)[at] = __float2bfloat16_rn(v);
   }
 }
 
@@ -375,8 +503,9 @@ cudaError_t launch_fwd(RopeArgs a, bool append, cudaStream_t stream, int* launch
   constexpr int HPW = 512 / D;
   const int groups = (a.q == nullptr ? 0 : (a.hq + HPW - 1) / HPW) + (append ? 2 : 1) * ((a.hkv + HPW - 1) / HPW);
   a.split = 1;
-  while (a.split * 2 <= groups && (int64_t)a.tokens * a.split < 32 * kSms) a.split *= 2;
-  const int64_t blocks = ((int64_t)a.tokens * a.split + kWarps - 1) / kWarps;
+  while (a.split * 2 <= groups && (int64_t)a.tokens * a.split < 32 * kSms && a.split < kWarps) a.split *= 2;
+  const int64_t need = ((int64_t)a.tokens * a.split + kWarps - 1) / kWarps;
+  const int64_t blocks = need < kFwdBlocks<T> * kSms ? need : kFwdBlocks<T> * kSms;
   if (blocks == 0) return cudaSuccess;
   if (append)
     norm_rope_kernel<T, D, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
@@ -386,14 +515,17 @@ cudaError_t launch_fwd(RopeArgs a, bool append, cudaStream_t stream, int* launch
   return cudaGetLastError();
 }
 
-// Blocks of the backward: at most kBwdBlocks, shared between queries and keys
-// by their heads.
-constexpr int kBwdBlocks = 4 * kSms;
+// Blocks of the backward: at most kBwdBlocks, shared between queries and keys by
+// their time: a token's angles cost about as much as 3/4 of a head group.
+constexpr int kBwdBlocks = 2 * kSms;
+template <typename T, int D>
 void bwd_blocks(int tokens, int hq, int hkv, int& nbq, int& nbk) {
+  constexpr int HPW = 512 / D;
+  const int all = kBwdPerSm<T> * kSms, cq = 4 * ((hq + HPW - 1) / HPW) + 3, ck = 4 * ((hkv + HPW - 1) / HPW) + 3;
   const int most = (tokens + kWarps - 1) / kWarps;
-  nbk = kBwdBlocks * hkv / (hq + hkv);
+  nbk = (all * ck + (cq + ck) / 2) / (cq + ck);
   nbk = nbk < 1 ? 1 : nbk;
-  nbq = kBwdBlocks - nbk;
+  nbq = all - nbk;
   nbq = nbq < most ? nbq : most;
   nbk = nbk < most ? nbk : most;
 }
@@ -402,16 +534,25 @@ template <typename T, int D>
 cudaError_t launch_bwd(const RopeArgs& a, const void* dq_out, const void* dk_out, void* dqw, void* dkw, float* part,
                        cudaStream_t stream, int* launches) {
   int nbq, nbk;
-  bwd_blocks(a.tokens, a.hq, a.hkv, nbq, nbk);
+  bwd_blocks<T, D>(a.tokens, a.hq, a.hkv, nbq, nbk);
   if (nbq + nbk > 0) {
     norm_rope_bwd_kernel<T, D><<<nbq + nbk, kThreads, 0, stream>>>(a, dq_out, dk_out, part, nbq);
     ++*launches;
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  norm_rope_dw_kernel<D><<<2, 1024, 0, stream>>>(part, nbq, nbk, dqw, dkw, a.weight_f32);
-  ++*launches;
-  return cudaGetLastError();
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(D / 32, 2);
+  c.blockDim = dim3(1024);
+  c.stream = stream;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, norm_rope_dw_kernel<D>, (const float*)part, nbq, nbk, dqw, dkw, a.weight_f32);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace
