@@ -61,28 +61,39 @@ struct PagedPlan {
   int64_t warp_sum[NT / 32];
 };
 
+// Whole block: exclusive prefix of v over its threads, and the sum.
+template <int NT>
+MOBA_DEV int64_t block_prefix(int64_t v, int64_t (&warp_sum)[NT / 32], int64_t& sum) {
+  const int t = threadIdx.x, lane = t & 31;
+  int64_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[t >> 5] = inc;
+  __syncthreads();
+  int64_t base = 0;
+  for (int i = 0; i < (t >> 5); ++i) base += warp_sum[i];
+  sum = base;
+  for (int i = t >> 5; i < NT / 32; ++i) sum += warp_sum[i];
+  __syncthreads();
+  return base + inc - v;
+}
+
 // Whole block of NT threads: fills the plan, returns W.
 template <int BR, int BK, int NT>
 MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
                             const PagedDims& dm) {
-  const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x, lane = t & 31;
+  const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
   int64_t w = 0;
   for (int b = t * per; b < min((t + 1) * per, dm.batch); ++b)
     w += paged_head_tiles<BR, BK>(paged_seq(cu, kv_len, dm, b), dm.G) * dm.hkv;
-  int64_t inc = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) p.warp_sum[t >> 5] = inc;
+  int64_t sum;
+  p.before[t] = block_prefix<NT>(w, p.warp_sum, sum);
+  if (t == 0) p.before[NT] = sum;
   __syncthreads();
-  int64_t base = 0;
-  for (int i = 0; i < (t >> 5); ++i) base += p.warp_sum[i];
-  p.before[t] = base + inc - w;
-  if (t == NT - 1) p.before[NT] = base + inc;
-  __syncthreads();
-  return p.before[NT];
+  return sum;
 }
 
 struct PagedItem {
@@ -137,6 +148,77 @@ MOBA_DEV void paged_next(PagedItem& it, const int32_t* __restrict__ cu, const in
     }
   }
   it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+}
+
+// Rounds of whole items.  Workers that go through items of one head at the same
+// pace share its keys in L2; workers at different places of them read the keys
+// again and again from memory.  So each worker first takes k whole items, item
+// r E + w in round r, and only the rest of the line is cut: worker w then takes
+// of it what is missing to its W / E tiles.  k is W / E over the largest item's
+// tiles (less one tile: every worker keeps a part of the rest, which the joining
+// of cut items counts on).
+template <int NT, int MAXE>
+struct PagedRounds {
+  int64_t items[NT + 1];      // items before the sequences of thread t
+  int64_t start[MAXE + 1];    // where the workers' parts of the rest begin, as positions in the line
+  unsigned long long whole[MAXE];
+  int rounds, largest;
+};
+
+template <int BR, int BK, int NT, int MAXE>
+MOBA_DEV PagedItem paged_locate_item(const PagedRounds<NT, MAXE>& r, int64_t at, const int32_t* __restrict__ cu,
+                                     const int32_t* __restrict__ kv_len, const PagedDims& dm) {
+  const int per = (dm.batch + NT - 1) / NT;
+  int lo = 0, hi = NT - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (r.items[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  PagedItem it;
+  int64_t off = at - r.items[lo];
+  int nrt = 0;
+  it.b = lo * per;
+  for (;; ++it.b) {
+    it.s = paged_seq(cu, kv_len, dm, it.b);
+    nrt = paged_row_tiles<BR>(it.s, dm.G);
+    if (off < (int64_t)nrt * dm.hkv || it.b + 1 >= dm.batch) break;
+    off -= (int64_t)nrt * dm.hkv;
+  }
+  it.h = (int)(off / nrt);
+  it.rt = (int)(off % nrt);
+  it.tile = 0;
+  it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+  return it;
+}
+
+// Whole block, after paged_plan.
+template <int BR, int BK, int NT, int MAXE>
+MOBA_DEV void paged_rounds(PagedRounds<NT, MAXE>& r, PagedPlan<NT>& p, int64_t W, int E, const int32_t* __restrict__ cu,
+                           const int32_t* __restrict__ kv_len, const PagedDims& dm) {
+  const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
+  if (t == 0) r.largest = 1;
+  for (int i = t; i < MAXE; i += NT) r.whole[i] = 0;
+  __syncthreads();
+  int64_t n = 0, sum;
+  int largest = 0;
+  for (int b = t * per; b < min((t + 1) * per, dm.batch); ++b) {
+    const PagedSeq s = paged_seq(cu, kv_len, dm, b);
+    const int nrt = paged_row_tiles<BR>(s, dm.G);
+    n += (int64_t)nrt * dm.hkv;
+    if (nrt > 0) largest = max(largest, paged_tiles<BR, BK>(s, dm.G, nrt - 1));
+  }
+  if (largest > 0) atomicMax(&r.largest, largest);
+  r.items[t] = block_prefix<NT>(n, p.warp_sum, sum);
+  if (t == 0) r.rounds = (int)((W / E - 1) / r.largest);
+  __syncthreads();
+  for (int64_t i = t; i < (int64_t)r.rounds * E; i += NT)
+    atomicAdd(&r.whole[i % E], (unsigned long long)paged_locate_item<BR, BK>(r, i, cu, kv_len, dm).tiles);
+  __syncthreads();
+  const int64_t mine = t < E ? (int64_t)r.whole[t] : 0;
+  const int64_t before = block_prefix<NT>(mine, p.warp_sum, sum);   // sum: the line up to the rest
+  if (t < E) r.start[t] = sum + t * W / E - before;
+  if (t == 0) r.start[E] = W;
+  __syncthreads();
 }
 
 // Workspace of a call: E headers, then the partial results.

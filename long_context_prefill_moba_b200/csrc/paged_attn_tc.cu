@@ -64,14 +64,22 @@ struct Geo {
   static constexpr int kRowBytes = 2 * D, kChunks = D / 8, kRowsPerOp = 32 / kChunks;
 };
 
+using Rounds = PagedRounds<kThreads, kWorkers>;
+
+// Where a role is in its CTA's work: whole items, then its part of the line's rest.
+struct PagedWalk {
+  PagedItem it;
+  int64_t pos;
+  int round;
+};
+
 struct Ctl {
   uint64_t q_full[2], k_full[2], v_full[2], v_fix[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], e_done[2];
   uint64_t f_full[4];
   uint64_t drain;
   uint32_t bad[4][4][4];   // [segment & 3][tile at the mask][32 keys each]: keys with non-finite values
   // where each softmax warp is in the line of tiles (kept here: the tile loop needs the registers)
-  PagedItem it[8];
-  int64_t pos[8];
+  PagedWalk walk[8];
   uint32_t tmem_base;
   int abort;
 };
@@ -127,6 +135,49 @@ MOBA_DEV Part make_part(const PagedItem& it, int64_t left, int G) {
   return p;
 }
 
+struct Line {
+  const PagedPlan<kThreads>& plan;
+  const Rounds& rounds;
+  const PagedArgs& a;
+  const PagedDims& dm;
+  int E, me;
+
+  MOBA_DEV int64_t stop() const { return rounds.start[me + 1]; }
+  MOBA_DEV bool more(const PagedWalk& k) const { return k.round < rounds.rounds || k.pos < stop(); }
+  MOBA_DEV void find(PagedWalk& k) const {
+    if (k.round < rounds.rounds)
+      k.it = paged_locate_item<kBR, kBK>(rounds, (int64_t)k.round * E + me, a.cu, a.kv_len, dm);
+    else if (k.pos < stop())
+      k.it = paged_locate<kBR, kBK, kThreads>(plan, k.pos, a.cu, a.kv_len, dm);
+  }
+  MOBA_DEV PagedWalk first() const {
+    PagedWalk k;
+    k.round = 0;
+    k.pos = rounds.start[me];
+    find(k);
+    return k;
+  }
+  MOBA_DEV Part part(const PagedWalk& k) const {
+    return make_part(k.it, k.round < rounds.rounds ? k.it.tiles : stop() - k.pos, dm.G);
+  }
+  MOBA_DEV void next(PagedWalk& k, int tiles) const {   // `tiles` of the part are done
+    if (k.round < rounds.rounds) {
+      ++k.round;
+      find(k);
+    } else {
+      k.pos += tiles;
+      if (k.pos < stop()) paged_next<kBR, kBK>(k.it, a.cu, a.kv_len, dm);
+    }
+  }
+  // workers of the item that this one begins at k.pos and does not end
+  MOBA_DEV int parts(const PagedWalk& k) const {
+    const int64_t end = k.pos + k.it.tiles;
+    int v = me + 1;
+    while (v < E && rounds.start[v] < end) ++v;
+    return v - me;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedArgs a, PagedDims dm,
@@ -135,18 +186,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   __shared__ PagedPlan<kThreads> plan;
+  __shared__ Rounds rounds;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::);
   const int64_t W = paged_plan<kBR, kBK, kThreads>(plan, a.cu, a.kv_len, dm);
-  const int64_t E = min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles);
-  const int64_t me = blockIdx.x;
+  const int E = (int)min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles), me = blockIdx.x;
   if (tid == 0) hdr[me].parts = 0;
   if (blockIdx.x == 0 && a.status != nullptr)
     for (int b = tid; b < dm.batch; b += kThreads)
       if (a.kv_len[b] > ((int64_t)dm.max_pages << dm.page_shift)) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
   if (me >= E) return;
-  const int64_t begin = me * W / E, stop = (me + 1) * W / E;
+  paged_rounds<kBR, kBK>(rounds, plan, W, E, a.cu, a.kv_len, dm);
+  const Line line{plan, rounds, a, dm, E, me};
 
   if (tid == 0) {
     for (int w = 0; w < 2; ++w) {
@@ -175,8 +227,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   tc_fence_after();
   const uint32_t tb = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
-  PagedItem it = paged_locate<kBR, kBK, kThreads>(plan, begin, a.cu, a.kv_len, dm);
-  int64_t pos = begin;
+  PagedWalk walk = line.first();
   int seg = 0;
 
   if (warp < 8)
@@ -194,10 +245,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const float sl2 = dm.scale_log2;
     int tiles = 0, mine = 0;   // tiles and items this row tile took part in
     bool ok = true;
-    if (lane == 0) {
-      ctl.it[warp] = it;
-      ctl.pos[warp] = begin;
-    }
+    if (lane == 0) ctl.walk[warp] = walk;
     __syncwarp();
     // the thread's row of the part: its token, head and the end of its keys; rows behind the last take part as if
     // they saw all keys (their queries are zero)
@@ -214,11 +262,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       r.lim = r.valid ? p.old + r.tok + 1 : 0x7fffffff;
       return r;
     };
-    for (; ctl.pos[warp] < (me + 1) * W / E && ok; ++seg) {
+    for (; line.more(ctl.walk[warp]) && ok; ++seg) {
       int t0, t1, lim;
       bool part_of;
       {
-        const Part p = make_part(ctl.it[warp], (me + 1) * W / E - ctl.pos[warp], dm.G);
+        const Part p = line.part(ctl.walk[warp]);
         const Row r = row_of(p);
         t0 = p.t0;
         t1 = p.t1;
@@ -333,7 +381,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                                                  mbar_wait(bar(&ctl.f_full[seg & 3]), (seg >> 2) & 1, abort_flag));
         if (ok) {
           tc_fence_after();
-          const Part p = make_part(ctl.it[warp], (me + 1) * W / E - ctl.pos[warp], dm.G);
+          const Part p = line.part(ctl.walk[warp]);
           const Row r = row_of(p);
           const bool valid = r.valid;
           const int tok = r.tok, head = r.head;
@@ -409,7 +457,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (valid) *reinterpret_cast<float2*>(part_ml + 2 * slot) = make_float2(m_used, l);
             if (begins && tid == 0) {
               PagedHeader h;
-              h.parts = paged_parts(ctl.pos[warp] + p.it.tiles, W, E, me);
+              h.parts = line.parts(ctl.walk[warp]);
               h.first = p.it.s.first;
               h.h = p.it.h;
               h.row0 = p.row0;
@@ -427,12 +475,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
       __syncwarp();
       if (lane == 0) {
-        PagedItem next = ctl.it[warp];
-        ctl.pos[warp] += t1 - t0;
-        if (ctl.pos[warp] < (me + 1) * W / E) {
-          paged_next<kBR, kBK>(next, a.cu, a.kv_len, dm);
-          ctl.it[warp] = next;
-        }
+        PagedWalk next = ctl.walk[warp];
+        line.next(next, t1 - t0);
+        ctl.walk[warp] = next;
       }
       __syncwarp();
     }
@@ -444,8 +489,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     int gt = 0, issued_k = 0, issued_v = 0;
     bool ok = true;
-    for (; pos < stop && ok; ++seg) {
-      const Part p = make_part(it, stop - pos, dm.G);
+    for (; line.more(walk) && ok; ++seg) {
+      const Part p = line.part(walk);
       const int32_t* row = a.table + (int64_t)p.it.b * dm.max_pages;
       const int have = (p.it.s.len + (1 << dm.page_shift) - 1) >> dm.page_shift;   // pages with keys
       // lanes hold 32 table entries, the next 32 on their way
@@ -496,8 +541,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         issued_v = gt + 1;
       }
-      pos += p.t1 - p.t0;
-      if (pos < stop) paged_next<kBR, kBK>(it, a.cu, a.kv_len, dm);
+      line.next(walk, p.t1 - p.t0);
     }
     if (*abort_flag) {
       // let the copies this warp issued land before the CTA exits
@@ -534,8 +578,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       };
       int gt = 0, mine[2] = {0, 0}, tiles[2] = {0, 0}, fixed[2] = {0, 0};
       bool ok = true;
-      for (; pos < stop && ok; ++seg) {
-        const Part p = make_part(it, stop - pos, dm.G);
+      for (; line.more(walk) && ok; ++seg) {
+        const Part p = line.part(walk);
         const int n = p.t1 - p.t0;
         ok = mbar_wait(bar(&ctl.k_full[gt & 1]), (gt >> 1) & 1, abort_flag) &&
              mbar_wait(bar(&ctl.q_full[0]), mine[0] & 1, abort_flag);
@@ -571,8 +615,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         ++mine[0];
         if (p.nq == 2) ++mine[1];
-        pos += n;
-        if (pos < stop) paged_next<kBR, kBK>(it, a.cu, a.kv_len, dm);
+        line.next(walk, n);
       }
       // every MMA this thread issued is complete before TMEM is released
       int never = 0;
@@ -584,8 +627,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int half = warp - 10;   // keys 64 half ..
     int gt = 0;
     bool ok = true;
-    for (; pos < stop && ok; ++seg) {
-      const Part p = make_part(it, stop - pos, dm.G);
+    for (; line.more(walk) && ok; ++seg) {
+      const Part p = line.part(walk);
       uint32_t(*bad)[4] = ctl.bad[seg & 3];
       if (lane < 8) bad[lane >> 1][2 * half + (lane & 1)] = 0;
       __syncwarp();
@@ -630,8 +673,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
       __syncwarp();
       if (ok) mbar_arrive(bar(&ctl.f_full[seg & 3]));
-      pos += p.t1 - p.t0;
-      if (pos < stop) paged_next<kBR, kBK>(it, a.cu, a.kv_len, dm);
+      line.next(walk, p.t1 - p.t0);
     }
   }
 
