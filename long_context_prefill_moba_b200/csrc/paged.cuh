@@ -35,23 +35,37 @@ MOBA_DEV PagedSeq paged_seq(const int32_t* __restrict__ cu, const int32_t* __res
 }
 
 // keys that the row tile [rt BR, ..) may see, in tiles; one tile at least, so
-// that rows that see nothing are written too
+// that rows that see nothing are written too.  (Rows of a call are below 2^31.)
 template <int BR, int BK>
 MOBA_DEV int paged_tiles(const PagedSeq& s, int G, int rt) {
-  const int64_t end = min((int64_t)s.n * G, (int64_t)(rt + 1) * BR);
-  const int last = (int)((end - 1) / G);
+  const uint32_t end = min((uint32_t)s.n * G, (uint32_t)(rt + 1) * BR);
+  const int last = (int)((end - 1) / (uint32_t)G);
   const int keys = max(s.len - s.n + last + 1, 0);
   return max((keys + BK - 1) / BK, 1);
 }
 template <int BR>
-MOBA_DEV int paged_row_tiles(const PagedSeq& s, int G) { return (int)(((int64_t)s.n * G + BR - 1) / BR); }
+MOBA_DEV int paged_row_tiles(const PagedSeq& s, int G) { return (int)(((uint32_t)s.n * G + BR - 1) / BR); }
 
-// tiles of one kv head of a sequence
+// tiles of one kv head of a sequence; the whole warp, each lane its own
+// sequence (n = 0: none).  Long sequences are summed by all lanes in turn.
 template <int BR, int BK>
 MOBA_DEV int64_t paged_head_tiles(const PagedSeq& s, int G) {
-  const int nrt = paged_row_tiles<BR>(s, G);
+  const int nrt = paged_row_tiles<BR>(s, G), lane = threadIdx.x & 31;
   int64_t w = 0;
-  for (int rt = 0; rt < nrt; ++rt) w += paged_tiles<BR, BK>(s, G, rt);
+  for (int rt = 0; rt < min(nrt, 4); ++rt) w += paged_tiles<BR, BK>(s, G, rt);
+  for (uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4); todo != 0; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    PagedSeq x;
+    x.first = 0;
+    x.n = __shfl_sync(0xffffffffu, s.n, src);
+    x.len = __shfl_sync(0xffffffffu, s.len, src);
+    const int m = __shfl_sync(0xffffffffu, nrt, src);
+    int64_t v = 0;
+    for (int rt = 4 + lane; rt < m; rt += 32) v += paged_tiles<BR, BK>(x, G, rt);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == src) w += v;
+  }
   return w;
 }
 
@@ -87,8 +101,12 @@ MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, co
                             const PagedDims& dm) {
   const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
   int64_t w = 0;
-  for (int b = t * per; b < min((t + 1) * per, dm.batch); ++b)
-    w += paged_head_tiles<BR, BK>(paged_seq(cu, kv_len, dm, b), dm.G) * dm.hkv;
+  for (int i = 0; i < per; ++i) {
+    const int b = t * per + i;
+    PagedSeq x = {0, 0, 0};
+    if (b < dm.batch) x = paged_seq(cu, kv_len, dm, b);
+    w += paged_head_tiles<BR, BK>(x, dm.G) * dm.hkv;
+  }
   int64_t sum;
   p.before[t] = block_prefix<NT>(w, p.warp_sum, sum);
   if (t == 0) p.before[NT] = sum;
@@ -102,11 +120,11 @@ struct PagedItem {
   PagedSeq s;
 };
 
-// the item that holds tile `at` of the line (at < W)
+// the item that holds tile `at` of the line (at < W); the whole warp, same `at`
 template <int BR, int BK, int NT>
 MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_t* __restrict__ cu,
                                 const int32_t* __restrict__ kv_len, const PagedDims& dm) {
-  const int per = (dm.batch + NT - 1) / NT;
+  const int per = (dm.batch + NT - 1) / NT, lane = threadIdx.x & 31;
   int lo = 0, hi = NT - 1;   // the last thread whose sequences begin at or before `at`
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -117,19 +135,33 @@ MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_
   it.b = lo * per;
   for (;; ++it.b) {
     it.s = paged_seq(cu, kv_len, dm, it.b);
-    head = paged_head_tiles<BR, BK>(it.s, dm.G);
+    const PagedSeq none = {0, 0, 0};
+    head = __shfl_sync(0xffffffffu, paged_head_tiles<BR, BK>(lane == 0 ? it.s : none, dm.G), 0);
     if (off < head * dm.hkv || it.b + 1 >= dm.batch) break;
     off -= head * dm.hkv;
   }
   it.h = (int)(off / head);
   off -= it.h * head;
-  for (it.rt = 0;; ++it.rt) {
-    it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
-    if (off < it.tiles) break;
-    off -= it.tiles;
+  // the row tile: 32 at a time, the first whose tiles reach beyond `off`
+  const int nrt = paged_row_tiles<BR>(it.s, dm.G);
+  for (it.rt = 0;; it.rt += 32) {
+    const int rt = it.rt + lane, mine = rt < nrt ? paged_tiles<BR, BK>(it.s, dm.G, rt) : 0;
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, off < inc);
+    if (hit != 0 || it.rt + 32 >= nrt) {
+      const int src = hit != 0 ? __ffs(hit) - 1 : 0;
+      it.rt += src;
+      it.tiles = __shfl_sync(0xffffffffu, mine, src);
+      it.tile = (int)(off - __shfl_sync(0xffffffffu, inc - mine, src));
+      return it;
+    }
+    off -= __shfl_sync(0xffffffffu, inc, 31);
   }
-  it.tile = (int)off;
-  return it;
 }
 
 // the item after a finished one; call only while tiles of the line are left

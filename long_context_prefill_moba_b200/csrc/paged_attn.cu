@@ -19,7 +19,8 @@ namespace moba {
 // at the headers of all its units at once: most are empty.  (One block an item,
 // its rows in turn, took 75 us to join 8 items of 74 parts and 80 us for items of
 // 256 rows.)
-constexpr int kCombineGrid = 148 * 8, kCombineThreads = 256;
+// a prime number of blocks: the units of a worker, E apart, meet in none
+constexpr int kCombineGrid = 1181, kCombineThreads = 256;
 
 template <typename T, int D, int kShare>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedHeader* __restrict__ hdr, int E, int BR,

@@ -9,7 +9,8 @@
 // keys.  Roles:
 //   warps 0-3  softmax for Q0        warps 4-7  softmax for Q1
 //   warp 8     TMA producer (and TMEM allocation)
-//   warp 9     tcgen05.mma issuer    warps 10-11  clean V tiles at the mask
+//   warp 9     tcgen05.mma issuer    warp 10    cleans V tiles at the mask
+//   warp 11    works out the CTA's parts, up to four ahead of the other roles
 // Per tile: S_w = Q_w K^T (SS MMA, fp32 in TMEM), the softmax warps turn it into
 // bf16 probabilities in place, O_w += P_w V (TS MMA).  The issue order PV0_i,
 // S0_{i+1}, PV1_i, S1_{i+1} keeps the tensor cores on one row tile while the
@@ -19,9 +20,9 @@
 // the pool; pages that are missing are fetched from behind the pool, which reads
 // as zeros and counts its bytes.  Slots behind a sequence's length may hold
 // anything, and a later token's value may be an infinity or NaN: 0 times it would
-// reach rows that do not see it.  Warps 10-11 therefore clear, in the tiles that
+// reach rows that do not see it.  Warp 10 therefore clears, in the tiles that
 // some row does not see whole, the slots behind the end and the non-finite
-// elements, and note the keys that had some; the epilogue adds those elements
+// elements, and notes the keys that had some; the epilogue adds those elements
 // to the rows that see them.
 //
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D) columns.
@@ -45,6 +46,7 @@ constexpr int kQT = 128, kBK = 128, kBR = 256;
 constexpr int kThreads = 384;
 constexpr int kWorkers = 148;            // one CTA an SM
 constexpr int kMinTiles = 2;
+constexpr int kReaders = 11;             // warps 0-10 read the planner's parts
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 64;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kServiceRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
@@ -66,7 +68,17 @@ struct Geo {
 
 using Rounds = PagedRounds<kThreads, kWorkers>;
 
-// Where a role is in its CTA's work: whole items, then its part of the line's rest.
+// a CTA's part of an item
+struct Part {
+  int b, h, first, len;   // sequence, kv head, row of its first new token, keys
+  int t0, t1, tiles;      // key tiles of the part, and of the item
+  int row0, rows, nq;     // nq = 0: the CTA's work is done
+  int old;                // position of the sequence's first new token
+  int fix0;               // first tile that some row does not see whole
+  int parts;              // workers of the item, where this part begins it and does not end it
+};
+
+// Where the planner is in its CTA's work: whole items, then its part of the line's rest.
 struct PagedWalk {
   PagedItem it;
   int64_t pos;
@@ -78,8 +90,8 @@ struct Ctl {
   uint64_t f_full[4];
   uint64_t drain;
   uint32_t bad[4][4][4];   // [segment & 3][tile at the mask][32 keys each]: keys with non-finite values
-  // where each softmax warp is in the line of tiles (kept here: the tile loop needs the registers)
-  PagedWalk walk[8];
+  uint64_t part_full[4], part_empty[4];
+  Part part[4];            // [segment & 3]
   uint32_t tmem_base;
   int abort;
 };
@@ -114,27 +126,7 @@ MOBA_DEV bool clear_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// a CTA's part of an item
-struct Part {
-  PagedItem it;
-  int t0, t1;       // key tiles
-  int row0, rows, nq;
-  int old;          // position of the sequence's first new token
-  int fix0;         // first tile that some row does not see whole
-};
-MOBA_DEV Part make_part(const PagedItem& it, int64_t left, int G) {
-  Part p;
-  p.it = it;
-  p.t0 = it.tile;
-  p.t1 = (int)min((int64_t)it.tiles, it.tile + left);
-  p.row0 = it.rt * kBR;
-  p.rows = (int)min((int64_t)kBR, (int64_t)it.s.n * G - p.row0);
-  p.nq = p.rows > kQT ? 2 : 1;
-  p.old = it.s.len - it.s.n;
-  p.fix0 = max(p.old + p.row0 / G + 1, 0) / kBK;
-  return p;
-}
-
+// The planner's view of the line of tiles (whole warp).
 struct Line {
   const PagedPlan<kThreads>& plan;
   const Rounds& rounds;
@@ -158,7 +150,28 @@ struct Line {
     return k;
   }
   MOBA_DEV Part part(const PagedWalk& k) const {
-    return make_part(k.it, k.round < rounds.rounds ? k.it.tiles : stop() - k.pos, dm.G);
+    const bool whole = k.round < rounds.rounds;
+    Part p;
+    p.b = k.it.b;
+    p.h = k.it.h;
+    p.first = k.it.s.first;
+    p.len = k.it.s.len;
+    p.tiles = k.it.tiles;
+    p.t0 = whole ? 0 : k.it.tile;
+    p.t1 = whole ? k.it.tiles : (int)min((int64_t)k.it.tiles, k.it.tile + (stop() - k.pos));
+    p.row0 = k.it.rt * kBR;
+    p.rows = (int)min((uint32_t)kBR, (uint32_t)k.it.s.n * dm.G - p.row0);
+    p.nq = p.rows > kQT ? 2 : 1;
+    p.old = k.it.s.len - k.it.s.n;
+    p.fix0 = max(p.old + p.row0 / dm.G + 1, 0) / kBK;
+    p.parts = 0;
+    if (p.t0 == 0 && p.t1 < p.tiles) {   // the workers whose parts of the rest begin before the item's end
+      const int64_t end = k.pos + p.tiles;
+      int v = me + 1;
+      while (v < E && rounds.start[v] < end) ++v;
+      p.parts = v - me;
+    }
+    return p;
   }
   MOBA_DEV void next(PagedWalk& k, int tiles) const {   // `tiles` of the part are done
     if (k.round < rounds.rounds) {
@@ -168,13 +181,6 @@ struct Line {
       k.pos += tiles;
       if (k.pos < stop()) paged_next<kBR, kBK>(k.it, a.cu, a.kv_len, dm);
     }
-  }
-  // workers of the item that this one begins at k.pos and does not end
-  MOBA_DEV int parts(const PagedWalk& k) const {
-    const int64_t end = k.pos + k.it.tiles;
-    int v = me + 1;
-    while (v < E && rounds.start[v] < end) ++v;
-    return v - me;
   }
 };
 
@@ -207,13 +213,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       mbar_init(bar(&ctl.e_done[w]), kQT);
       mbar_init(bar(&ctl.k_full[w]), 1);
       mbar_init(bar(&ctl.v_full[w]), 1);
-      mbar_init(bar(&ctl.v_fix[w]), 64);
+      mbar_init(bar(&ctl.v_fix[w]), 32);
       mbar_init(bar(&ctl.k_free[w]), 1);
-      mbar_init(bar(&ctl.v_free[w]), 3);   // the MMAs that read it, and warps 10 and 11
+      mbar_init(bar(&ctl.v_free[w]), 2);   // the MMAs that read it, and warp 10
       mbar_init(bar(&ctl.s_full[w]), 1);
       mbar_init(bar(&ctl.o_full[w]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(&ctl.f_full[i]), 64);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(&ctl.f_full[i]), 32);
+      mbar_init(bar(&ctl.part_full[i]), 1);
+      mbar_init(bar(&ctl.part_empty[i]), kReaders);
+    }
     mbar_init(bar(&ctl.drain), 1);
     ctl.abort = 0;
     fence_mbar_init();
@@ -227,8 +237,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   tc_fence_after();
   const uint32_t tb = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
-  PagedWalk walk = line.first();
+  // the CTA's parts one after another: the planner's next one is waited for and given back by each reading warp
   int seg = 0;
+  auto await_part = [&]() { return mbar_wait(bar(&ctl.part_full[seg & 3]), (seg >> 2) & 1, abort_flag); };
+  auto done_part = [&]() { mbar_arrive(bar(&ctl.part_empty[seg & 3])); };
 
   if (warp < 8)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
@@ -245,8 +257,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const float sl2 = dm.scale_log2;
     int tiles = 0, mine = 0;   // tiles and items this row tile took part in
     bool ok = true;
-    if (lane == 0) ctl.walk[warp] = walk;
-    __syncwarp();
     // the thread's row of the part: its token, head and the end of its keys; rows behind the last take part as if
     // they saw all keys (their queries are zero)
     struct Row {
@@ -258,23 +268,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       r.valid = w * kQT + rho < p.rows;
       const int row = p.row0 + w * kQT + rho;
       r.tok = r.valid ? row / dm.G : 0;
-      r.head = p.it.h * dm.G + (r.valid ? row % dm.G : 0);
+      r.head = p.h * dm.G + (r.valid ? row % dm.G : 0);
       r.lim = r.valid ? p.old + r.tok + 1 : 0x7fffffff;
       return r;
     };
-    for (; line.more(ctl.walk[warp]) && ok; ++seg) {
-      int t0, t1, lim;
-      bool part_of;
+    for (;; ++seg) {
+      ok = __all_sync(0xffffffffu, await_part());
+      if (!ok) break;
+      const Part& p = ctl.part[seg & 3];
+      if (p.nq == 0) break;
+      const int t0 = p.t0, t1 = p.t1;
+      const bool part_of = w < p.nq;
+      int lim;
       {
-        const Part p = line.part(ctl.walk[warp]);
         const Row r = row_of(p);
-        t0 = p.t0;
-        t1 = p.t1;
         lim = r.lim;
-        part_of = w < p.nq;
         if (part_of) {
           const bool valid = r.valid;
-          const int64_t qrow = (int64_t)(p.it.s.first + r.tok) * dm.q_stride + (int64_t)r.head * D;
+          const int64_t qrow = (int64_t)(p.first + r.tok) * dm.q_stride + (int64_t)r.head * D;
         {
           const int wrow0 = (warp & 3) * 32, cc = lane % Gm::kChunks;
 #pragma unroll
@@ -381,11 +392,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                                                  mbar_wait(bar(&ctl.f_full[seg & 3]), (seg >> 2) & 1, abort_flag));
         if (ok) {
           tc_fence_after();
-          const Part p = line.part(ctl.walk[warp]);
           const Row r = row_of(p);
           const bool valid = r.valid;
           const int tok = r.tok, head = r.head;
-          const bool begins = p.t0 == 0, ends = p.t1 == p.it.tiles;
+          const bool begins = p.t0 == 0, ends = p.t1 == p.tiles;
           const uint32_t(*bad)[4] = ctl.bad[seg & 3];
           uint32_t some = 0;
 #pragma unroll
@@ -396,10 +406,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               for (uint32_t bits = bad[i >> 2][i & 3]; bits != 0; bits &= bits - 1) {
                 const int u = (p.fix0 + (i >> 2)) * kBK + (i & 3) * 32 + __ffs(bits) - 1;
                 if (!valid || u >= lim) continue;
-                const int64_t page = a.table[(int64_t)p.it.b * dm.max_pages + (u >> dm.page_shift)];
+                const int64_t page = a.table[(int64_t)p.b * dm.max_pages + (u >> dm.page_shift)];
                 if (page < 0 || page >= dm.num_pages) continue;
                 const __nv_bfloat16* v = (const __nv_bfloat16*)a.v_pool + page * dm.v_page_stride +
-                                         (((int64_t)p.it.h << dm.page_shift) + (u & ((1 << dm.page_shift) - 1))) * D + cc * 32;
+                                         (((int64_t)p.h << dm.page_shift) + (u & ((1 << dm.page_shift) - 1))) * D + cc * 32;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   const float x = to_f32(v[e]);
@@ -426,7 +436,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                              pack_bf16x2(__uint_as_float(o[8 * e8 + 6]) * inv, __uint_as_float(o[8 * e8 + 7]) * inv));
             }
             __syncwarp();
-            const int64_t orow = (int64_t)(p.it.s.first + tok) * dm.hq + head;
+            const int64_t orow = (int64_t)(p.first + tok) * dm.hq + head;
             const int cc = lane % Gm::kChunks;
 #pragma unroll
             for (int k2 = 0; k2 < 32 / Gm::kRowsPerOp; ++k2) {
@@ -437,7 +447,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               if (vd) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + rd * D + cc * 8) = x;
             }
             if (valid && a.lse != nullptr)
-              a.lse[(size_t)head * dm.tokens + p.it.s.first + tok] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+              a.lse[(size_t)head * dm.tokens + p.first + tok] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
           } else {
             const size_t slot = (size_t)(begins ? 2 * me + 1 : 2 * me) * kBR + w * kQT + rho;
 #pragma unroll
@@ -457,9 +467,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (valid) *reinterpret_cast<float2*>(part_ml + 2 * slot) = make_float2(m_used, l);
             if (begins && tid == 0) {
               PagedHeader h;
-              h.parts = line.parts(ctl.walk[warp]);
-              h.first = p.it.s.first;
-              h.h = p.it.h;
+              h.parts = p.parts;
+              h.first = p.first;
+              h.h = p.h;
               h.row0 = p.row0;
               h.rows = p.rows;
               h.pad[0] = h.pad[1] = h.pad[2] = 0;
@@ -473,13 +483,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         ++mine;
       }
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        PagedWalk next = ctl.walk[warp];
-        line.next(next, t1 - t0);
-        ctl.walk[warp] = next;
-      }
-      __syncwarp();
+      if (lane == 0) done_part();
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -489,10 +495,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     int gt = 0, issued_k = 0, issued_v = 0;
     bool ok = true;
-    for (; line.more(walk) && ok; ++seg) {
-      const Part p = line.part(walk);
-      const int32_t* row = a.table + (int64_t)p.it.b * dm.max_pages;
-      const int have = (p.it.s.len + (1 << dm.page_shift) - 1) >> dm.page_shift;   // pages with keys
+    for (;; ++seg) {
+      ok = __all_sync(0xffffffffu, await_part());
+      if (!ok) break;
+      const Part p = ctl.part[seg & 3];
+      if (p.nq == 0) break;
+      const int32_t* row = a.table + (int64_t)p.b * dm.max_pages;
+      const int have = (p.len + (1 << dm.page_shift) - 1) >> dm.page_shift;   // pages with keys
       // lanes hold 32 table entries, the next 32 on their way
       auto entries = [&](int first) {
         const int i = first + lane;
@@ -526,7 +535,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const int page = __shfl_sync(0xffffffffu, cur, ((u0 + r) >> dm.page_shift) - first);
           const int y = (u0 + r) & ((1 << dm.page_shift) - 1);
           if (lane < Gm::kHalves)
-            tma_load_4d(ks + lane * kHalf + r * 128, &tmK, 64 * lane, y, p.it.h, page, bar(&ctl.k_full[s]));
+            tma_load_4d(ks + lane * kHalf + r * 128, &tmK, 64 * lane, y, p.h, page, bar(&ctl.k_full[s]));
         }
         issued_k = gt + 1;
         if (gt >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(&ctl.v_free[s]), ((gt >> 1) - 1) & 1, abort_flag));
@@ -537,11 +546,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const int page = __shfl_sync(0xffffffffu, cur, ((u0 + r) >> dm.page_shift) - first);
           const int y = (u0 + r) & ((1 << dm.page_shift) - 1);
           if (lane < Gm::kHalves)
-            tma_load_4d(vs + lane * kHalf + r * 128, &tmV, 64 * lane, y, p.it.h, page, bar(&ctl.v_full[s]));
+            tma_load_4d(vs + lane * kHalf + r * 128, &tmV, 64 * lane, y, p.h, page, bar(&ctl.v_full[s]));
         }
         issued_v = gt + 1;
       }
-      line.next(walk, p.t1 - p.t0);
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) done_part();
     }
     if (*abort_flag) {
       // let the copies this warp issued land before the CTA exits
@@ -578,9 +589,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       };
       int gt = 0, mine[2] = {0, 0}, tiles[2] = {0, 0}, fixed[2] = {0, 0};
       bool ok = true;
-      for (; line.more(walk) && ok; ++seg) {
-        const Part p = line.part(walk);
-        const int n = p.t1 - p.t0;
+      for (;; ++seg) {
+        ok = await_part();
+        if (!ok) break;
+        const struct { int t0, nq, fix0; } p = {ctl.part[seg & 3].t0, ctl.part[seg & 3].nq, ctl.part[seg & 3].fix0};
+        if (p.nq == 0) break;
+        const int n = ctl.part[seg & 3].t1 - p.t0;
         ok = mbar_wait(bar(&ctl.k_full[gt & 1]), (gt >> 1) & 1, abort_flag) &&
              mbar_wait(bar(&ctl.q_full[0]), mine[0] & 1, abort_flag);
         if (!ok) break;
@@ -615,64 +629,83 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         ++mine[0];
         if (p.nq == 2) ++mine[1];
-        line.next(walk, n);
+        if (!ok) break;
+        done_part();
       }
       // every MMA this thread issued is complete before TMEM is released
       int never = 0;
       mma_commit(bar(&ctl.drain));
       mbar_wait(bar(&ctl.drain), 0, &never);
     }
-  } else {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ V tiles at the mask
-    const int half = warp - 10;   // keys 64 half ..
     int gt = 0;
     bool ok = true;
-    for (; line.more(walk) && ok; ++seg) {
-      const Part p = line.part(walk);
-      uint32_t(*bad)[4] = ctl.bad[seg & 3];
-      if (lane < 8) bad[lane >> 1][2 * half + (lane & 1)] = 0;
+    for (;; ++seg) {
+      ok = __all_sync(0xffffffffu, await_part());
+      if (!ok) break;
+      const int t0 = ctl.part[seg & 3].t0, t1 = ctl.part[seg & 3].t1, fix0 = ctl.part[seg & 3].fix0,
+                len = ctl.part[seg & 3].len;
+      if (ctl.part[seg & 3].nq == 0) break;
+      uint32_t* bad = &ctl.bad[seg & 3][0][0];
+      if (lane < 16) bad[lane] = 0;
       __syncwarp();
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++gt) {
+      for (int t = t0; t < t1; ++t, ++gt) {
         // every tile is waited for and released here, whether it needs cleaning or not: a role that skipped tiles
         // would lose count of the barrier's phases
         const int s = gt & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(&ctl.v_full[s]), (gt >> 1) & 1, abort_flag));
         if (!ok) break;
-        if (t < p.fix0) {
-          if (lane == 0) mbar_arrive(bar(&ctl.v_free[s]));
-          continue;
-        }
-        const uint32_t vs = base + Gm::kOffV + s * Gm::kTile;
+        if (t >= fix0) {
+          const uint32_t vs = base + Gm::kOffV + s * Gm::kTile;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 32 + lane;
+            const bool behind = t * kBK + r >= len;
+            bool odd = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = half * 64 + i * 32 + lane;
-          const bool behind = t * kBK + r >= p.it.s.len;
-          bool odd = false;
-#pragma unroll
-          for (int c = 0; c < Gm::kChunks; ++c) {
-            const uint32_t at = vs + (c >> 3) * kHalf + sw128_off(r, c & 7);
-            if (behind) {
-              st_shared_v4(at, 0, 0, 0, 0);
-            } else {
-              uint4 x = ld_shared_v4(at);
-              const bool b0 = clear_nonfinite(x.x), b1 = clear_nonfinite(x.y), b2 = clear_nonfinite(x.z),
-                         b3 = clear_nonfinite(x.w);
-              if (b0 || b1 || b2 || b3) {
-                st_shared_v4(at, x.x, x.y, x.z, x.w);
-                odd = true;
+            for (int c = 0; c < Gm::kChunks; ++c) {
+              const uint32_t at = vs + (c >> 3) * kHalf + sw128_off(r, c & 7);
+              if (behind) {
+                st_shared_v4(at, 0, 0, 0, 0);
+              } else {
+                uint4 x = ld_shared_v4(at);
+                const bool b0 = clear_nonfinite(x.x), b1 = clear_nonfinite(x.y), b2 = clear_nonfinite(x.z),
+                           b3 = clear_nonfinite(x.w);
+                if (b0 || b1 || b2 || b3) {
+                  st_shared_v4(at, x.x, x.y, x.z, x.w);
+                  odd = true;
+                }
               }
             }
+            const uint32_t word = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) bad[(t - fix0) * 4 + i] = word;
           }
-          const uint32_t word = __ballot_sync(0xffffffffu, odd);
-          if (lane == 0) bad[t - p.fix0][2 * half + i] = word;
+          fence_proxy_async_smem();
+          mbar_arrive(bar(&ctl.v_fix[s]));
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(&ctl.v_fix[s]));
-        __syncwarp();
         if (lane == 0) mbar_arrive(bar(&ctl.v_free[s]));
       }
+      if (!ok) break;
       __syncwarp();
-      if (ok) mbar_arrive(bar(&ctl.f_full[seg & 3]));
+      mbar_arrive(bar(&ctl.f_full[seg & 3]));
+      if (lane == 0) done_part();
+    }
+  } else {
+    // ------------------------------------------------------------ planner
+    PagedWalk walk = line.first();
+    for (;; ++seg) {
+      const bool ok = seg < 4 || mbar_wait(bar(&ctl.part_empty[seg & 3]), ((seg >> 2) - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const bool more = line.more(walk);
+      Part p = {};
+      if (more) p = line.part(walk);
+      if (lane == 0) {
+        ctl.part[seg & 3] = p;
+        mbar_arrive(bar(&ctl.part_full[seg & 3]));
+      }
+      if (!more) break;
       line.next(walk, p.t1 - p.t0);
     }
   }
