@@ -36,23 +36,25 @@ MOBA_DEV PagedSeq paged_seq(const int32_t* __restrict__ cu, const int32_t* __res
 
 // keys that the row tile [rt BR, ..) may see, in tiles; one tile at least, so
 // that rows that see nothing are written too.  (Rows of a call are below 2^31.)
-template <int BR, int BK>
+// X is an item's fixed cost in tiles: the line counts it as tiles at the item's
+// start that hold no keys.
+template <int BR, int BK, int X>
 MOBA_DEV int paged_tiles(const PagedSeq& s, int G, int rt) {
   const uint32_t end = min((uint32_t)s.n * G, (uint32_t)(rt + 1) * BR);
   const int last = (int)((end - 1) / (uint32_t)G);
   const int keys = max(s.len - s.n + last + 1, 0);
-  return max((keys + BK - 1) / BK, 1);
+  return max((keys + BK - 1) / BK, 1) + X;
 }
 template <int BR>
 MOBA_DEV int paged_row_tiles(const PagedSeq& s, int G) { return (int)(((uint32_t)s.n * G + BR - 1) / BR); }
 
 // tiles of one kv head of a sequence; the whole warp, each lane its own
 // sequence (n = 0: none).  Long sequences are summed by all lanes in turn.
-template <int BR, int BK>
+template <int BR, int BK, int X>
 MOBA_DEV int64_t paged_head_tiles(const PagedSeq& s, int G) {
   const int nrt = paged_row_tiles<BR>(s, G), lane = threadIdx.x & 31;
   int64_t w = 0;
-  for (int rt = 0; rt < min(nrt, 4); ++rt) w += paged_tiles<BR, BK>(s, G, rt);
+  for (int rt = 0; rt < min(nrt, 4); ++rt) w += paged_tiles<BR, BK, X>(s, G, rt);
   for (uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4); todo != 0; todo &= todo - 1) {
     const int src = __ffs(todo) - 1;
     PagedSeq x;
@@ -61,7 +63,7 @@ MOBA_DEV int64_t paged_head_tiles(const PagedSeq& s, int G) {
     x.len = __shfl_sync(0xffffffffu, s.len, src);
     const int m = __shfl_sync(0xffffffffu, nrt, src);
     int64_t v = 0;
-    for (int rt = 4 + lane; rt < m; rt += 32) v += paged_tiles<BR, BK>(x, G, rt);
+    for (int rt = 4 + lane; rt < m; rt += 32) v += paged_tiles<BR, BK, X>(x, G, rt);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == src) w += v;
@@ -96,7 +98,7 @@ MOBA_DEV int64_t block_prefix(int64_t v, int64_t (&warp_sum)[NT / 32], int64_t& 
 }
 
 // Whole block of NT threads: fills the plan, returns W.
-template <int BR, int BK, int NT>
+template <int BR, int BK, int X, int NT>
 MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
                             const PagedDims& dm) {
   const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
@@ -105,7 +107,7 @@ MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, co
     const int b = t * per + i;
     PagedSeq x = {0, 0, 0};
     if (b < dm.batch) x = paged_seq(cu, kv_len, dm, b);
-    w += paged_head_tiles<BR, BK>(x, dm.G) * dm.hkv;
+    w += paged_head_tiles<BR, BK, X>(x, dm.G) * dm.hkv;
   }
   int64_t sum;
   p.before[t] = block_prefix<NT>(w, p.warp_sum, sum);
@@ -121,7 +123,7 @@ struct PagedItem {
 };
 
 // the item that holds tile `at` of the line (at < W); the whole warp, same `at`
-template <int BR, int BK, int NT>
+template <int BR, int BK, int X, int NT>
 MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_t* __restrict__ cu,
                                 const int32_t* __restrict__ kv_len, const PagedDims& dm) {
   const int per = (dm.batch + NT - 1) / NT, lane = threadIdx.x & 31;
@@ -136,7 +138,7 @@ MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_
   for (;; ++it.b) {
     it.s = paged_seq(cu, kv_len, dm, it.b);
     const PagedSeq none = {0, 0, 0};
-    head = __shfl_sync(0xffffffffu, paged_head_tiles<BR, BK>(lane == 0 ? it.s : none, dm.G), 0);
+    head = __shfl_sync(0xffffffffu, paged_head_tiles<BR, BK, X>(lane == 0 ? it.s : none, dm.G), 0);
     if (off < head * dm.hkv || it.b + 1 >= dm.batch) break;
     off -= head * dm.hkv;
   }
@@ -145,7 +147,7 @@ MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_
   // the row tile: 32 at a time, the first whose tiles reach beyond `off`
   const int nrt = paged_row_tiles<BR>(it.s, dm.G);
   for (it.rt = 0;; it.rt += 32) {
-    const int rt = it.rt + lane, mine = rt < nrt ? paged_tiles<BR, BK>(it.s, dm.G, rt) : 0;
+    const int rt = it.rt + lane, mine = rt < nrt ? paged_tiles<BR, BK, X>(it.s, dm.G, rt) : 0;
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,7 +167,7 @@ MOBA_DEV PagedItem paged_locate(const PagedPlan<NT>& p, int64_t at, const int32_
 }
 
 // the item after a finished one; call only while tiles of the line are left
-template <int BR, int BK>
+template <int BR, int BK, int X>
 MOBA_DEV void paged_next(PagedItem& it, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
                          const PagedDims& dm) {
   it.tile = 0;
@@ -179,7 +181,7 @@ MOBA_DEV void paged_next(PagedItem& it, const int32_t* __restrict__ cu, const in
       } while (it.s.n == 0 && it.b + 1 < dm.batch);
     }
   }
-  it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+  it.tiles = paged_tiles<BR, BK, X>(it.s, dm.G, it.rt);
 }
 
 // Rounds of whole items.  Workers that go through items of one head at the same
@@ -197,7 +199,7 @@ struct PagedRounds {
   int rounds, largest;
 };
 
-template <int BR, int BK, int NT, int MAXE>
+template <int BR, int BK, int X, int NT, int MAXE>
 MOBA_DEV PagedItem paged_locate_item(const PagedRounds<NT, MAXE>& r, int64_t at, const int32_t* __restrict__ cu,
                                      const int32_t* __restrict__ kv_len, const PagedDims& dm) {
   const int per = (dm.batch + NT - 1) / NT;
@@ -219,12 +221,12 @@ MOBA_DEV PagedItem paged_locate_item(const PagedRounds<NT, MAXE>& r, int64_t at,
   it.h = (int)(off / nrt);
   it.rt = (int)(off % nrt);
   it.tile = 0;
-  it.tiles = paged_tiles<BR, BK>(it.s, dm.G, it.rt);
+  it.tiles = paged_tiles<BR, BK, X>(it.s, dm.G, it.rt);
   return it;
 }
 
 // Whole block, after paged_plan.
-template <int BR, int BK, int NT, int MAXE>
+template <int BR, int BK, int X, int NT, int MAXE>
 MOBA_DEV void paged_rounds(PagedRounds<NT, MAXE>& r, PagedPlan<NT>& p, int64_t W, int E, const int32_t* __restrict__ cu,
                            const int32_t* __restrict__ kv_len, const PagedDims& dm) {
   const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
@@ -237,14 +239,14 @@ MOBA_DEV void paged_rounds(PagedRounds<NT, MAXE>& r, PagedPlan<NT>& p, int64_t W
     const PagedSeq s = paged_seq(cu, kv_len, dm, b);
     const int nrt = paged_row_tiles<BR>(s, dm.G);
     n += (int64_t)nrt * dm.hkv;
-    if (nrt > 0) largest = max(largest, paged_tiles<BR, BK>(s, dm.G, nrt - 1));
+    if (nrt > 0) largest = max(largest, paged_tiles<BR, BK, X>(s, dm.G, nrt - 1));
   }
   if (largest > 0) atomicMax(&r.largest, largest);
   r.items[t] = block_prefix<NT>(n, p.warp_sum, sum);
   if (t == 0) r.rounds = (int)((W / E - 1) / r.largest);
   __syncthreads();
   for (int64_t i = t; i < (int64_t)r.rounds * E; i += NT)
-    atomicAdd(&r.whole[i % E], (unsigned long long)paged_locate_item<BR, BK>(r, i, cu, kv_len, dm).tiles);
+    atomicAdd(&r.whole[i % E], (unsigned long long)paged_locate_item<BR, BK, X>(r, i, cu, kv_len, dm).tiles);
   __syncthreads();
   const int64_t mine = t < E ? (int64_t)r.whole[t] : 0;
   const int64_t before = block_prefix<NT>(mine, p.warp_sum, sum);   // sum: the line up to the rest

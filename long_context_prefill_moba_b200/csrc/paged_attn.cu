@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
   __shared__ float sa[kVecWarps][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::);
-  const int64_t W = paged_plan<R, kVecBK, kVecThreads>(plan, a.cu, a.kv_len, dm);
+  const int64_t W = paged_plan<R, kVecBK, 0, kVecThreads>(plan, a.cu, a.kv_len, dm);
   const int64_t E = min((int64_t)vec_workers(R), (W + kVecMinTiles - 1) / kVecMinTiles);
   const int64_t w = (int64_t)blockIdx.x * kVecWarps + warp;
   if (lane == 0) hdr[w].parts = 0;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
   const int myrow = lane / LPR;
   int64_t pos = w * W / E;
   const int64_t stop = (w + 1) * W / E;
-  PagedItem it = paged_locate<R, kVecBK, kVecThreads>(plan, pos, a.cu, a.kv_len, dm);
+  PagedItem it = paged_locate<R, kVecBK, 0, kVecThreads>(plan, pos, a.cu, a.kv_len, dm);
 
   while (pos < stop) {
     const int t0 = it.tile, t1 = (int)min((int64_t)it.tiles, it.tile + (stop - pos));
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
       }
     }
     pos += t1 - t0;
-    if (pos < stop) paged_next<R, kVecBK>(it, a.cu, a.kv_len, dm);
+    if (pos < stop) paged_next<R, kVecBK, 0>(it, a.cu, a.kv_len, dm);
   }
 }
 

@@ -45,7 +45,12 @@ using namespace sm100;
 constexpr int kQT = 128, kBK = 128, kBR = 256;
 constexpr int kThreads = 384;
 constexpr int kWorkers = 148;            // one CTA an SM
-constexpr int kMinTiles = 2;
+constexpr int kMinTiles = 4;
+// What an item costs beside its tiles (2.1 us each): its queries' load, the
+// cleaning at the mask and the epilogue take some 6 us.  With no cost counted,
+// the workers of a short prompt's first items ended after 92 us and those of its
+// last after 50.
+constexpr int kItemCost = 3;
 constexpr int kReaders = 11;             // warps 0-10 read the planner's parts
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 64;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kServiceRegs <= kThreads * kLaunchRegs,
@@ -74,7 +79,7 @@ struct Part {
   int t0, t1, tiles;      // key tiles of the part, and of the item
   int row0, rows, nq;     // nq = 0: the CTA's work is done
   int old;                // position of the sequence's first new token
-  int fix0;               // first tile that some row does not see whole
+  int all, fix0;          // keys that every row sees; the first tile that has others
   int parts;              // workers of the item, where this part begins it and does not end it
 };
 
@@ -118,12 +123,10 @@ MOBA_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, in
       : "memory");
 }
 
-// the non-finite halves of a packed pair cleared; true if there was one
-MOBA_DEV bool clear_nonfinite(uint32_t& w) {
-  const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
-  if (lo) w &= 0xffff0000u;
-  if (hi) w &= 0x0000ffffu;
-  return lo || hi;
+// the non-finite halves of a packed pair cleared
+MOBA_DEV void clear_nonfinite(uint32_t& w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
 }
 
 // The planner's view of the line of tiles (whole warp).
@@ -138,9 +141,9 @@ struct Line {
   MOBA_DEV bool more(const PagedWalk& k) const { return k.round < rounds.rounds || k.pos < stop(); }
   MOBA_DEV void find(PagedWalk& k) const {
     if (k.round < rounds.rounds)
-      k.it = paged_locate_item<kBR, kBK>(rounds, (int64_t)k.round * E + me, a.cu, a.kv_len, dm);
+      k.it = paged_locate_item<kBR, kBK, kItemCost>(rounds, (int64_t)k.round * E + me, a.cu, a.kv_len, dm);
     else if (k.pos < stop())
-      k.it = paged_locate<kBR, kBK, kThreads>(plan, k.pos, a.cu, a.kv_len, dm);
+      k.it = paged_locate<kBR, kBK, kItemCost, kThreads>(plan, k.pos, a.cu, a.kv_len, dm);
   }
   MOBA_DEV PagedWalk first() const {
     PagedWalk k;
@@ -156,30 +159,31 @@ struct Line {
     p.h = k.it.h;
     p.first = k.it.s.first;
     p.len = k.it.s.len;
-    p.tiles = k.it.tiles;
-    p.t0 = whole ? 0 : k.it.tile;
-    p.t1 = whole ? k.it.tiles : (int)min((int64_t)k.it.tiles, k.it.tile + (stop() - k.pos));
+    p.tiles = k.it.tiles - kItemCost;
+    p.t0 = whole ? 0 : max(k.it.tile - kItemCost, 0);
+    p.t1 = whole ? p.tiles : (int)min((int64_t)k.it.tiles, k.it.tile + (stop() - k.pos)) - kItemCost;
     p.row0 = k.it.rt * kBR;
     p.rows = (int)min((uint32_t)kBR, (uint32_t)k.it.s.n * dm.G - p.row0);
     p.nq = p.rows > kQT ? 2 : 1;
     p.old = k.it.s.len - k.it.s.n;
-    p.fix0 = max(p.old + p.row0 / dm.G + 1, 0) / kBK;
+    p.all = p.old + p.row0 / dm.G + 1;
+    p.fix0 = max(p.all, 0) / kBK;
     p.parts = 0;
     if (p.t0 == 0 && p.t1 < p.tiles) {   // the workers whose parts of the rest begin before the item's end
-      const int64_t end = k.pos + p.tiles;
+      const int64_t end = k.pos - k.it.tile + k.it.tiles;
       int v = me + 1;
       while (v < E && rounds.start[v] < end) ++v;
       p.parts = v - me;
     }
     return p;
   }
-  MOBA_DEV void next(PagedWalk& k, int tiles) const {   // `tiles` of the part are done
+  MOBA_DEV void next(PagedWalk& k) const {
     if (k.round < rounds.rounds) {
       ++k.round;
       find(k);
     } else {
-      k.pos += tiles;
-      if (k.pos < stop()) paged_next<kBR, kBK>(k.it, a.cu, a.kv_len, dm);
+      k.pos += k.it.tiles - k.it.tile;
+      if (k.pos < stop()) paged_next<kBR, kBK, kItemCost>(k.it, a.cu, a.kv_len, dm);
     }
   }
 };
@@ -196,14 +200,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::);
-  const int64_t W = paged_plan<kBR, kBK, kThreads>(plan, a.cu, a.kv_len, dm);
+  const int64_t W = paged_plan<kBR, kBK, kItemCost, kThreads>(plan, a.cu, a.kv_len, dm);
   const int E = (int)min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles), me = blockIdx.x;
   if (tid == 0) hdr[me].parts = 0;
   if (blockIdx.x == 0 && a.status != nullptr)
     for (int b = tid; b < dm.batch; b += kThreads)
       if (a.kv_len[b] > ((int64_t)dm.max_pages << dm.page_shift)) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
   if (me >= E) return;
-  paged_rounds<kBR, kBK>(rounds, plan, W, E, a.cu, a.kv_len, dm);
+  paged_rounds<kBR, kBK, kItemCost>(rounds, plan, W, E, a.cu, a.kv_len, dm);
   const Line line{plan, rounds, a, dm, E, me};
 
   if (tid == 0) {
@@ -645,7 +649,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ok = __all_sync(0xffffffffu, await_part());
       if (!ok) break;
       const int t0 = ctl.part[seg & 3].t0, t1 = ctl.part[seg & 3].t1, fix0 = ctl.part[seg & 3].fix0,
-                len = ctl.part[seg & 3].len;
+                len = ctl.part[seg & 3].len, all = ctl.part[seg & 3].all;
       if (ctl.part[seg & 3].nq == 0) break;
       uint32_t* bad = &ctl.bad[seg & 3][0][0];
       if (lane < 16) bad[lane] = 0;
@@ -658,28 +662,38 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) break;
         if (t >= fix0) {
           const uint32_t vs = base + Gm::kOffV + s * Gm::kTile;
+          // keys from `all` on are not seen by every row; the ones before need no cleaning
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 32 + lane;
+          for (int r0 = max(all - t * kBK, 0) & ~31; r0 < kBK; r0 += 32) {
+            const int r = r0 + lane;
             const bool behind = t * kBK + r >= len;
-            bool odd = false;
+            // the largest exponent field decides (as magnitudes, 16-bit integers order like the values)
+            uint32_t m = 0;
+            if (behind) {
 #pragma unroll
-            for (int c = 0; c < Gm::kChunks; ++c) {
-              const uint32_t at = vs + (c >> 3) * kHalf + sw128_off(r, c & 7);
-              if (behind) {
-                st_shared_v4(at, 0, 0, 0, 0);
-              } else {
-                uint4 x = ld_shared_v4(at);
-                const bool b0 = clear_nonfinite(x.x), b1 = clear_nonfinite(x.y), b2 = clear_nonfinite(x.z),
-                           b3 = clear_nonfinite(x.w);
-                if (b0 || b1 || b2 || b3) {
-                  st_shared_v4(at, x.x, x.y, x.z, x.w);
-                  odd = true;
-                }
+              for (int c = 0; c < Gm::kChunks; ++c) st_shared_v4(vs + (c >> 3) * kHalf + sw128_off(r, c & 7), 0, 0, 0, 0);
+            } else {
+#pragma unroll
+              for (int c = 0; c < Gm::kChunks; ++c) {
+                const uint4 x = ld_shared_v4(vs + (c >> 3) * kHalf + sw128_off(r, c & 7));
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
               }
             }
+            const bool odd = (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
             const uint32_t word = __ballot_sync(0xffffffffu, odd);
-            if (lane == 0) bad[(t - fix0) * 4 + i] = word;
+            if (word != 0) {
+              if (odd) {
+#pragma unroll 1
+                for (int c = 0; c < Gm::kChunks; ++c) {
+                  const uint32_t at = vs + (c >> 3) * kHalf + sw128_off(r, c & 7);
+                  uint4 x = ld_shared_v4(at);
+                  clear_nonfinite(x.x); clear_nonfinite(x.y); clear_nonfinite(x.z); clear_nonfinite(x.w);
+                  st_shared_v4(at, x.x, x.y, x.z, x.w);
+                }
+              }
+              if (lane == 0) bad[(t - fix0) * 4 + (r0 >> 5)] = word;
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(bar(&ctl.v_fix[s]));
@@ -698,15 +712,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (;; ++seg) {
       const bool ok = seg < 4 || mbar_wait(bar(&ctl.part_empty[seg & 3]), ((seg >> 2) - 1) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const bool more = line.more(walk);
       Part p = {};
-      if (more) p = line.part(walk);
+      if (line.more(walk)) p = line.part(walk);
+      // a part that ends within an item's fixed cost has no keys: the next worker begins the item
+      const bool more = p.nq != 0 && p.t1 > p.t0;
+      if (!more) p.nq = 0;
       if (lane == 0) {
         ctl.part[seg & 3] = p;
         mbar_arrive(bar(&ctl.part_full[seg & 3]));
       }
       if (!more) break;
-      line.next(walk, p.t1 - p.t0);
+      line.next(walk);
     }
   }
 

@@ -92,7 +92,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     fence_mbar_init();
   }
   if (tid == 0) abort_word = 0;
-  const int64_t W = paged_plan<kBR, kBK, kThreads>(plan, a.cu, a.kv_len, dm);   // two block barriers
+  const int64_t W = paged_plan<kBR, kBK, 0, kThreads>(plan, a.cu, a.kv_len, dm);   // two block barriers
   const int64_t E = min((int64_t)workers(D), (W + kMinTiles - 1) / kMinTiles);
   const int64_t me = (int64_t)blockIdx.x * kPairs + pair;
   volatile int* abort_flag = &abort_word;
@@ -103,7 +103,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   if (me >= E) return;
   const int64_t stop = (me + 1) * W / E;
   int64_t pos = me * W / E;
-  PagedItem it = paged_locate<kBR, kBK, kThreads>(plan, pos, a.cu, a.kv_len, dm);
+  PagedItem it = paged_locate<kBR, kBK, 0, kThreads>(plan, pos, a.cu, a.kv_len, dm);
   const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + pair * Gm::kRing;
 
   if (warp >= kPairs) {
@@ -153,7 +153,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
       }
       pos += t1 - it.tile;
-      if (pos < stop) paged_next<kBR, kBK>(it, a.cu, a.kv_len, dm);
+      if (pos < stop) paged_next<kBR, kBK, 0>(it, a.cu, a.kv_len, dm);
     }
     // the copies outlive neither the consumer nor this warp
     for (int i = n > kStages ? n - kStages : 0; i < n && ok; ++i)
@@ -366,7 +366,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
     }
     pos += t1 - t0;
-    if (pos < stop) paged_next<kBR, kBK>(it, a.cu, a.kv_len, dm);
+    if (pos < stop) paged_next<kBR, kBK, 0>(it, a.cu, a.kv_len, dm);
   }
 }
 
