@@ -399,6 +399,8 @@ cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int 
 size_t paged_decode_ws(int d);
 cudaError_t launch_paged_decode(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
 size_t paged_tc_ws(int d);
+size_t paged_f32_ws(int d);
+cudaError_t launch_paged_f32(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
 cudaError_t launch_paged_tc(const PagedDims& dm, int d, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches);
 
 size_t paged_attn_ws(int dtype, int d) {
@@ -406,7 +408,7 @@ size_t paged_attn_ws(int dtype, int d) {
     const size_t a = paged_tc_ws(d), b = paged_decode_ws(d);
     return a > b ? a : b;
   }
-  size_t most = 0;
+  size_t most = paged_f32_ws(d);
   for (int R : {4, 8}) {
     const size_t b = paged_ws_bytes(vec_workers(R), R, d);
     most = most > b ? most : b;
@@ -417,10 +419,11 @@ size_t paged_attn_ws(int dtype, int d) {
 cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const PagedArgs& a, void* ws, cudaStream_t stream,
                               int* launches) {
   if (dm.tokens == 0) return cudaSuccess;
-  if (dtype == MOBA_BF16) {
-    if ((int64_t)dm.tokens * dm.G > 16 * (int64_t)dm.batch) return launch_paged_tc(dm, d, a, ws, stream, launches);
-    return launch_paged_decode(dm, d, a, ws, stream, launches);
-  }
+  // few rows a kv head of a sequence: the cache's bytes bound the call; many: the products
+  const bool few = (int64_t)dm.tokens * dm.G <= 16 * (int64_t)dm.batch;
+  if (dtype == MOBA_BF16)
+    return few ? launch_paged_decode(dm, d, a, ws, stream, launches) : launch_paged_tc(dm, d, a, ws, stream, launches);
+  if (!few) return launch_paged_f32(dm, d, a, ws, stream, launches);
   return d == 128 ? launch_vec_rows<float, 128>(dm, a, ws, stream, launches)
                   : launch_vec_rows<float, 64>(dm, a, ws, stream, launches);
 }
