@@ -204,17 +204,18 @@ MOBA_DEV int seq_of_token(const int32_t* __restrict__ cu, int batch, int t, int 
   return min(lo + c, batch - 1);
 }
 
-// Head groups loaded ahead of the one in work: 2 of bf16 (1 KB each), 1 of fp32.
-// At one, warps waited for their loads 60% of the time.
-template <typename T> constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
-template <typename T> constexpr int kFwdBlocks = sizeof(T) == 2 ? 3 : 2;   // an SM, for 80 and 128 registers
+// Blocks an SM: the registers of a thread against the warps that hide each
+// other's waits.  bf16, 32768 tokens: 4 blocks of 64 registers, one head group
+// loaded ahead of the one in work, take 112 us; 3 blocks of 80 with one ahead
+// 119, with two 125, with three 121; 2 blocks with two to four ahead 140 to 149.
+template <typename T> constexpr int kFwdBlocks = sizeof(T) == 2 ? 4 : 3;
 
 // A warp takes tokens in a stride (or every split-th head group of them, where
 // there are few tokens) as one run of head groups, loads running ahead across
 // tokens.
 template <typename T, int D, bool kAppend>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks<T>) norm_rope_kernel(RopeArgs a) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH, kRing = kAhead<T> + 1;
+  constexpr int LPH = D / 16, HPW = 32 / LPH, kRing = 2;   // a head group in work, one on its way
   __shared__ Angles<LPH> cs_all[kWarps];
   __shared__ ulonglong2 sm_w[2][4][LPH];   // weights of queries and keys as lane j reads them
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
