@@ -67,8 +67,10 @@ struct Geo {
   static constexpr uint32_t kTile = kBK * D * 2;
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile;
-  static constexpr uint32_t kSmem = 6 * kTile + 1024;
-  static constexpr int kRowBytes = 2 * D, kChunks = D / 8, kRowsPerOp = 32 / kChunks;
+  // output rows on their way out, 32 channels of a warp's 32 rows
+  static constexpr uint32_t kOffOut = 6 * kTile, kOutWarp = 32 * 64;
+  static constexpr uint32_t kSmem = kOffOut + 8 * kOutWarp + 1024;
+  static constexpr int kChunks = D / 8, kRowsPerOp = 32 / kChunks;
 };
 
 using Rounds = PagedRounds<kThreads, kWorkers>;
@@ -91,7 +93,7 @@ struct PagedWalk {
 };
 
 struct Ctl {
-  uint64_t q_full[2], k_full[2], v_full[2], v_fix[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], e_done[2];
+  uint64_t q_full[2], k_full[2], v_full[2], v_fix[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2];
   uint64_t f_full[4];
   uint64_t drain;
   uint32_t bad[4][4][4];   // [segment & 3][tile at the mask][32 keys each]: keys with non-finite values
@@ -103,10 +105,9 @@ struct Ctl {
 
 MOBA_DEV uint32_t bar(const uint64_t* b) { return smem_u32(b); }
 
-template <int D>
-MOBA_DEV uint32_t stage_off(int rr, int c) {
-  return (uint32_t)(rr * Geo<D>::kRowBytes + ((c ^ (rr & (Geo<D>::kChunks - 1))) << 4));
-}
+// 16-byte chunk c of row rr in the output staging (64-byte rows): a quarter-warp's
+// rows, and a row's chunks, lie in different banks
+MOBA_DEV uint32_t stage_off(int rr, int c) { return (uint32_t)(rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)); }
 MOBA_DEV void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -214,7 +215,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(&ctl.q_full[w]), kQT);
       mbar_init(bar(&ctl.p_full[w]), kQT);
-      mbar_init(bar(&ctl.e_done[w]), kQT);
       mbar_init(bar(&ctl.k_full[w]), 1);
       mbar_init(bar(&ctl.v_full[w]), 1);
       mbar_init(bar(&ctl.v_fix[w]), 32);
@@ -276,38 +276,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       r.lim = r.valid ? p.old + r.tok + 1 : 0x7fffffff;
       return r;
     };
+    // the warp's 32 query rows of a part, whole rows a copy instruction
+    auto load_q = [&](const Part& p) {
+      const Row r = row_of(p);
+      const int64_t qrow = (int64_t)(p.first + r.tok) * dm.q_stride + (int64_t)r.head * D;
+      const int wrow0 = (warp & 3) * 32, cc = lane % Gm::kChunks;
+#pragma unroll
+      for (int k2 = 0; k2 < 32 / Gm::kRowsPerOp; ++k2) {
+        const int rl = Gm::kRowsPerOp * k2 + lane / Gm::kChunks;
+        const int64_t rs = __shfl_sync(0xffffffffu, (long long)qrow, rl);
+        const bool vs = __shfl_sync(0xffffffffu, r.valid, rl);
+        cp_async16(qs + (cc >> 3) * kHalf + sw128_off(wrow0 + rl, cc & 7), (const __nv_bfloat16*)a.q + (vs ? rs : 0) + cc * 8, vs);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(bar(&ctl.q_full[w]));
+    };
+    bool loaded = false;   // this part's queries, while the last part ended
     for (;; ++seg) {
       ok = __all_sync(0xffffffffu, await_part());
       if (!ok) break;
       const Part& p = ctl.part[seg & 3];
       if (p.nq == 0) break;
-      const int t0 = p.t0, t1 = p.t1;
-      const bool part_of = w < p.nq;
-      int lim;
-      {
-        const Row r = row_of(p);
-        lim = r.lim;
-        if (part_of) {
-          const bool valid = r.valid;
-          const int64_t qrow = (int64_t)(p.first + r.tok) * dm.q_stride + (int64_t)r.head * D;
-        {
-          const int wrow0 = (warp & 3) * 32, cc = lane % Gm::kChunks;
-#pragma unroll
-          for (int k2 = 0; k2 < 32 / Gm::kRowsPerOp; ++k2) {
-            const int rl = Gm::kRowsPerOp * k2 + lane / Gm::kChunks;
-            const int64_t rs = __shfl_sync(0xffffffffu, (long long)qrow, rl);
-            const bool vs = __shfl_sync(0xffffffffu, valid, rl);
-            cp_async16(qs + (cc >> 3) * kHalf + sw128_off(wrow0 + rl, cc & 7), (const __nv_bfloat16*)a.q + (vs ? rs : 0) + cc * 8,
-                       vs);
-          }
-        }
-        }
-      }
-      if (part_of) {
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        mbar_arrive(bar(&ctl.q_full[w]));
+      const int t0 = p.t0, t1 = p.t1, lim = row_of(p).lim;
+      if (w < p.nq) {
+        if (!loaded) load_q(p);
+        loaded = false;
         float m_used = -INFINITY, l = 0.f;
         auto load_s = [&](uint32_t (&sr)[128], int t) {
           tmem_ld32(tS + 0, sr);
@@ -392,6 +387,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           tc_fence_before();
           mbar_arrive(bar(&ctl.p_full[w]));
         }
+        if (ok) {
+          // the last S is complete: the next part's queries take their place while PV runs
+          ++seg;
+          ok = __all_sync(0xffffffffu, await_part());
+          loaded = ok && w < ctl.part[seg & 3].nq;
+          if (loaded) load_q(ctl.part[seg & 3]);
+          --seg;
+        }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(&ctl.o_full[w]), mine & 1, abort_flag) &&
                                                  mbar_wait(bar(&ctl.f_full[seg & 3]), (seg >> 2) & 1, abort_flag));
         if (ok) {
@@ -424,7 +427,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           };
           if (begins && ends) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const uint32_t stg = base + Gm::kOffQ + (uint32_t)warp * (32u * Gm::kRowBytes);
+            const uint32_t stg = base + Gm::kOffOut + (uint32_t)warp * Gm::kOutWarp;
+            const int64_t orow = (int64_t)(p.first + tok) * dm.hq + head;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t o[32];
@@ -433,22 +437,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               if (some) add_bad(o, cc);
 #pragma unroll
               for (int e8 = 0; e8 < 4; ++e8)
-                st_shared_v4(stg + stage_off<D>(lane, cc * 4 + e8),
+                st_shared_v4(stg + stage_off(lane, e8),
                              pack_bf16x2(__uint_as_float(o[8 * e8 + 0]) * inv, __uint_as_float(o[8 * e8 + 1]) * inv),
                              pack_bf16x2(__uint_as_float(o[8 * e8 + 2]) * inv, __uint_as_float(o[8 * e8 + 3]) * inv),
                              pack_bf16x2(__uint_as_float(o[8 * e8 + 4]) * inv, __uint_as_float(o[8 * e8 + 5]) * inv),
                              pack_bf16x2(__uint_as_float(o[8 * e8 + 6]) * inv, __uint_as_float(o[8 * e8 + 7]) * inv));
-            }
-            __syncwarp();
-            const int64_t orow = (int64_t)(p.first + tok) * dm.hq + head;
-            const int cc = lane % Gm::kChunks;
+              __syncwarp();
 #pragma unroll
-            for (int k2 = 0; k2 < 32 / Gm::kRowsPerOp; ++k2) {
-              const int rl = Gm::kRowsPerOp * k2 + lane / Gm::kChunks;
-              const int64_t rd = __shfl_sync(0xffffffffu, (long long)orow, rl);
-              const bool vd = __shfl_sync(0xffffffffu, valid, rl);
-              const uint4 x = ld_shared_v4(stg + stage_off<D>(rl, cc));
-              if (vd) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + rd * D + cc * 8) = x;
+              for (int k2 = 0; k2 < 4; ++k2) {
+                const int rl = 8 * k2 + (lane >> 2);
+                const int64_t rd = __shfl_sync(0xffffffffu, (long long)orow, rl);
+                const bool vd = __shfl_sync(0xffffffffu, valid, rl);
+                const uint4 x = ld_shared_v4(stg + stage_off(rl, lane & 3));
+                if (vd) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + rd * D + cc * 32 + (lane & 3) * 8) = x;
+              }
+              __syncwarp();
             }
             if (valid && a.lse != nullptr)
               a.lse[(size_t)head * dm.tokens + p.first + tok] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
@@ -480,10 +483,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               hdr[me] = h;
             }
           }
-          // O is read, and the row tile's staging over: its buffers may take the next item's queries
-          tc_fence_before();
-          mbar_arrive(bar(&ctl.e_done[w]));
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(&ctl.e_done[w]), mine & 1, abort_flag));
+          tc_fence_before();   // O is read: the next P this warp hands over orders it before the next PV
         }
         ++mine;
       }
