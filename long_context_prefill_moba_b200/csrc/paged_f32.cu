@@ -13,6 +13,8 @@
 // Keys and values arrive by cp.async, one tile ahead; slots behind the
 // sequence's end are filled with zeros, and in tiles that some row does not see
 // whole a value meets only the rows that see it (0 times an infinity is not 0).
+#include <type_traits>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_f32_kernel(PagedArgs a, Pag
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int i = 0; i < KPT; ++i) s[r][i] = 0;
-#pragma unroll 4
+#pragma unroll 16
       for (int c = 0; c < D; c += 4) {
         ulonglong2 q[4], k[KPT];
 #pragma unroll
@@ -170,29 +172,33 @@ __global__ void __launch_bounds__(kThreads, 2) paged_f32_kernel(PagedArgs a, Pag
         }
       }
       __syncwarp();
-#pragma unroll 2
-      for (int u = 0; u < BK; u += 4) {
-        float4 p[4];
+      // o += P V; in tiles that some row does not see whole, key by key as the rows see them
+      auto add_pv = [&](auto whole) {
+#pragma unroll 4
+        for (int u = 0; u < BK; u += 4) {
+          float4 p[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * Gm::kPRow + u);
+          for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * Gm::kPRow + u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ulonglong2 v[C4];
+          for (int e = 0; e < 4; ++e) {
+            ulonglong2 v[C4];
 #pragma unroll
-          for (int c = 0; c < C4; ++c) v[c] = *reinterpret_cast<const ulonglong2*>(vt + (u + e) * Gm::kRow + 4 * tx + 32 * c);
+            for (int c = 0; c < C4; ++c) v[c] = *reinterpret_cast<const ulonglong2*>(vt + (u + e) * Gm::kRow + 4 * tx + 32 * c);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = e == 0 ? p[r].x : e == 1 ? p[r].y : e == 2 ? p[r].z : p[r].w;
-            if (masked && t * BK + u + e >= lim[r]) continue;
-            const uint64_t x2 = f2_pack(x, x);
+            for (int r = 0; r < 4; ++r) {
+              const float x = e == 0 ? p[r].x : e == 1 ? p[r].y : e == 2 ? p[r].z : p[r].w;
+              if (!decltype(whole)::value && t * BK + u + e >= lim[r]) continue;
+              const uint64_t x2 = f2_pack(x, x);
 #pragma unroll
-            for (int c = 0; c < C4; ++c) {
-              o[r][2 * c] = f2_fma(x2, v[c].x, o[r][2 * c]);
-              o[r][2 * c + 1] = f2_fma(x2, v[c].y, o[r][2 * c + 1]);
+              for (int c = 0; c < C4; ++c) {
+                o[r][2 * c] = f2_fma(x2, v[c].x, o[r][2 * c]);
+                o[r][2 * c + 1] = f2_fma(x2, v[c].y, o[r][2 * c + 1]);
+              }
             }
           }
         }
-      }
+      };
+      if (masked) add_pv(std::false_type()); else add_pv(std::true_type());
       __syncthreads();   // the tile, and with the last one the queries, may be overwritten
     }
 
