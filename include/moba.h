@@ -469,7 +469,7 @@ typedef struct {
 } moba_paged_shape_t;
 
 /* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31,
- * max_pages * page_size < 2^31). */
+ * max_pages * page_size <= 2^30). */
 MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* shape);
 
 /* Appends the step's keys and values to the cache, keys (and queries, where
@@ -501,13 +501,15 @@ MOBA_API size_t moba_paged_attn_workspace_size(const moba_paged_shape_t* shape);
  * decode step; any mix of lengths is one call.
  *   q [T, hq, d]     dtype, token stride as in shape                  (read)
  *   k_pool, v_pool   (read)
- *   out [T, hq, d]   dtype, dense                                     (written)
+ *   out [T, hq, d]   dtype, dense, apart from q                       (written)
  *   lse [hq, T] fp32, natural log, or NULL                            (written)
  *   ws    >= moba_paged_attn_workspace_size bytes of device scratch; calls that
  *         overlap on the GPU need one each
  * A row that sees no key (position < 0), or whose weights are all zero, gives
  * out = 0 and lse = -infinity.  Keys and values that a row does not see do not
- * reach it, infinities and NaN among them.  Results are bitwise reproducible.
+ * reach it, infinities and NaN among them.  Results are bitwise reproducible from
+ * call to call; where a sequence's keys are cut into parts, and so the last bits
+ * of its rows, depends on the other sequences of the call.
  * *status becomes MOBA_ERR_TIMEOUT if a bounded device-side wait of a
  * tensor-core kernel expired (out is then invalid). */
 MOBA_API moba_status_t moba_paged_attn(const moba_paged_shape_t* shape, const void* q, const void* k_pool,

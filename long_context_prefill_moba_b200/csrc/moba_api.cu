@@ -161,6 +161,7 @@ moba::RopeArgs rope_shape_args(const moba_rope_shape_t* s) {
   return a;
 }
 
+constexpr int64_t kMaxPagedKeys = 1ll << 30;   // positions and tile borders stay in 32 bits
 int64_t page_dense(const moba_paged_shape_t* s) { return (int64_t)s->hkv * s->page_size * s->head_dim; }
 int page_shift(const moba_paged_shape_t* s) {
   int sh = 0;
@@ -721,7 +722,7 @@ MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* s) {
       !stride_ok(s->v_page_stride, page_dense(s), es))
     return MOBA_ERR_INVALID_ARG;
   if (s->batch > kGridYZMax || (int64_t)s->tokens * s->hq > kI32Max ||
-      (int64_t)s->max_pages * s->page_size > kI32Max)
+      (int64_t)s->max_pages * s->page_size > kMaxPagedKeys)
     return MOBA_ERR_UNSUPPORTED;
   return MOBA_OK;
 }

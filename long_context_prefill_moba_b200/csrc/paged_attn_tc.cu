@@ -710,7 +710,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // ------------------------------------------------------------ planner
     PagedWalk walk = line.first();
     for (;; ++seg) {
-      const bool ok = seg < 4 || mbar_wait(bar(&ctl.part_empty[seg & 3]), ((seg >> 2) - 1) & 1, abort_flag);
+      // the readers may be at work on the four parts before for longer than the other waits last (2 s are some 10^8
+      // keys): up to 32 times that, unless one of them gave up
+      bool ok = seg < 4;
+      for (int i = 0; i < 32 && !ok && !*abort_flag; ++i) {
+        int late = 0;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(&ctl.part_empty[seg & 3]), ((seg >> 2) - 1) & 1, &late));
+      }
       if (!__all_sync(0xffffffffu, ok)) break;
       Part p = {};
       if (line.more(walk)) p = line.part(walk);

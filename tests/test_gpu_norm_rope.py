@@ -186,6 +186,29 @@ def test_zero_rows_extremes_and_in_place(cuda_device):
     assert torch.equal(torch.nan_to_num(x), torch.nan_to_num(q_out)) and torch.equal(torch.nan_to_num(k), torch.nan_to_num(k_out))
 
 
+def test_layouts_that_are_copied(cuda_device):
+    """Heads before tokens, every second token, one token for all: as dense inputs, gradients in the inputs' layout."""
+    import long_context_prefill_moba_b200 as M
+    dev = cuda_device
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    w, f = 1 + 0.3 * n(64), M.moba_rope_inv_freq(32, device=dev)
+    pos = torch.arange(12, dtype=torch.int32, device=dev)
+    for q, k in ((n(2, 4, 6, 64).transpose(1, 2), n(2, 2, 6, 64).transpose(1, 2)), (n(24, 4, 64)[::2], n(24, 2, 64)[::2]),
+                 (n(1, 4, 64).expand(12, 4, 64), n(1, 2, 64).expand(12, 2, 64))):
+        dense = [x.contiguous().requires_grad_() for x in (q, k)]
+        want = M.moba_norm_rope(*dense, w, w, pos, f)
+        leaves = [x.detach().requires_grad_() for x in (q, k)]
+        got = M.moba_norm_rope(*leaves, w, w, pos, f)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        d = [n(*x.shape) for x in want]
+        a, b = torch.autograd.grad(got, leaves, d), torch.autograd.grad(want, dense, d)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        one = torch.autograd.grad(M.moba_norm_rope(*leaves, w, w, pos, f)[1].sum(), leaves)   # an expanded gradient; none for q
+        assert (one[0] == 0).all() and torch.isfinite(one[1]).all()
+
+
 def test_no_tokens(cuda_device):
     import long_context_prefill_moba_b200 as M
     dev = cuda_device

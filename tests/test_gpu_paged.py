@@ -143,7 +143,12 @@ def test_attention(cuda_device, case):
     ([(3, 3)] * 200 + [(4000, 4100)] + [(70, 400)] * 30, 128, 6, 2, 128, "bf16"),
     ([(300, 2000), (200, 300)], 64, 8, 8, 128, "f32"),
     ([(1, 40000), (1, 90000)], 64, 8, 2, 128, "bf16"),
-    ([(1, 40000), (2, 30000)], 64, 8, 2, 64, "f32")],
+    ([(1, 40000), (2, 30000)], 64, 8, 2, 64, "f32"),
+    ([(20, 25 + i % 9) if i % 4 else (0, 3) for i in range(1000)], 16, 2, 2, 64, "bf16"),
+    ([(20, 25 + i % 9) if i % 4 else (0, 3) for i in range(400)], 16, 2, 2, 64, "f32"),
+    ([(1, 30 + i % 50) for i in range(900)], 16, 4, 1, 64, "f32"),
+    ([(3, 700), (260, 900)], 32, 512, 1, 64, "bf16"),
+    ([(1, 700), (1, 1500)], 32, 300, 1, 128, "bf16")],
     ids=lambda c: f"{c[5]}-d{c[4]}-{c[2]}x{c[3]}-p{c[1]}-{len(c[0])}seq-{c[0][0]}")
 def test_attention_of_many_tiles(cuda_device, case):
     """Enough keys that every worker goes through many tiles and several items: rows at every border and random ones."""
@@ -159,6 +164,42 @@ def test_attention_of_many_tiles(cuda_device, case):
     few = cu if len(cu) < 20 else cu[::25]
     rows = {int(x) for x in list(few) + [x - 1 for x in few] + list(r.randint(0, c.total, 25)) if 0 <= x < c.total}
     check_attention(c, q, out, lse, rows=rows)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 50])
+def test_sequences_that_share_pages(cuda_device, dt, new):
+    """One prompt's pages in two tables, and one page twice in a table."""
+    import long_context_prefill_moba_b200 as M
+    c = Cache([(new, 64 + new), (new, 64 + new)], 16, 2, 64, dt, cuda_device)
+    q = c.rand(new, 4, 64).repeat(2, 1, 1)
+    cu, kv_len, table = (x.clone() for x in c.index)
+    table[1] = table[0]
+    out, lse = M.moba_cache_attention(q, c.k_pool, c.v_pool, cu, kv_len, table, return_lse=True)
+    # (where a sequence's keys are cut depends on the others of the call: equal within the bounds, not to the bit)
+    c.table = table.cpu()
+    check_attention(c, q, out, lse)
+    table[:, 1] = table[:, 0]
+    c.table = table.cpu()
+    out, lse = M.moba_cache_attention(q, c.k_pool, c.v_pool, cu, kv_len, table, return_lse=True)
+    check_attention(c, q, out, lse)
+
+
+def test_only_padding(cuda_device):
+    """A step in which no sequence has a new token: nothing is written."""
+    import long_context_prefill_moba_b200 as M
+    for dt in ("bf16", "f32"):
+        for rows in (2, 40):
+            c = Cache([(0, 50), (0, 0)], 16, 2, 64, dt, cuda_device, pad=rows, nan=False)
+            x = c.rand(rows, 8, 64)
+            out = torch.full((rows, 4, 64), 7.0, dtype=c.dtype, device=cuda_device)
+            before = c.k_pool.clone()
+            M.moba_cache_attention(x[:, :4], c.k_pool, c.v_pool, *c.index, out=out)
+            M.moba_cache_append(x[:, 4:6], x[:, 6:], *c.index, c.k_pool, c.v_pool, q=x[:, :4], q_out=out)
+            assert (out == 7.0).all() and torch.equal(c.k_pool, before)
+            none = torch.empty(0, 4, 64, dtype=c.dtype, device=cuda_device)
+            assert M.moba_cache_attention(none, c.k_pool, c.v_pool, *c.index).shape == (0, 4, 64)
+            assert M.moba_cache_append(none[:, :2], none[:, 2:], *c.index, c.k_pool, c.v_pool, q=none).shape == (0, 4, 64)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])

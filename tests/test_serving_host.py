@@ -68,7 +68,8 @@ def test_rope_flags_out_of_range(L):
     (dict(k_page_stride=2 * 64 * 128 - 8), INVALID), (dict(v_page_stride=2 * 64 * 128 + 4), INVALID),
     (dict(v_stride=100), INVALID), (dict(k_stride=260), INVALID),
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED),
-    (dict(batch=65536), UNSUPPORTED), (dict(max_pages=1 << 25), UNSUPPORTED), (dict(tokens=1 << 29), UNSUPPORTED)])
+    (dict(batch=65536), UNSUPPORTED), (dict(max_pages=1 << 25), UNSUPPORTED),
+    (dict(max_pages=1 << 24), OK), (dict(max_pages=(1 << 24) + 1), UNSUPPORTED), (dict(tokens=1 << 29), UNSUPPORTED)])
 def test_paged_shapes(L, kw, want):
     s = paged_shape(**kw)
     assert M.moba_check_paged_shape(s) == want
