@@ -358,10 +358,15 @@ cudaError_t launch_vec(const PagedDims& dm, const PagedArgs& a, void* ws, cudaSt
   return launch_paged_combine(sizeof(T) == 2 ? MOBA_BF16 : MOBA_F32, D, l, kE, R, a, dm, stream, launches);
 }
 
+// 4 rows a warp leave room for twice the warps, 8 read a key for twice the rows.
+// head_dim 128, 32K keys: 1 row of 16 heads takes 105 us with 4 rows a warp and
+// 128 with 8, 4 rows of 8 heads 75 and 80; 32 sequences of 2.5K keys with 8 rows
+// 166 and 157, with 32 rows 449 and 369.  head_dim 64 with 8 rows: 99 and 123.
 template <typename T, int D>
 cudaError_t launch_vec_rows(const PagedDims& dm, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches) {
-  if ((int64_t)dm.tokens * dm.G <= 4 * (int64_t)dm.batch) return launch_vec<T, D, 4>(dm, a, ws, stream, launches);
-  return launch_vec<T, D, 8>(dm, a, ws, stream, launches);
+  if constexpr (D == 128)
+    if ((int64_t)dm.tokens * dm.G > 4 * (int64_t)dm.batch) return launch_vec<T, D, 8>(dm, a, ws, stream, launches);
+  return launch_vec<T, D, 4>(dm, a, ws, stream, launches);
 }
 
 }  // namespace
@@ -419,8 +424,12 @@ size_t paged_attn_ws(int dtype, int d) {
 cudaError_t launch_paged_attn(const PagedDims& dm, int dtype, int d, const PagedArgs& a, void* ws, cudaStream_t stream,
                               int* launches) {
   if (dm.tokens == 0) return cudaSuccess;
-  // few rows a kv head of a sequence: the cache's bytes bound the call; many: the products
-  const bool few = (int64_t)dm.tokens * dm.G <= 16 * (int64_t)dm.batch;
+  // Rows of a kv head's group a sequence, on average: with few, reading the cache
+  // bounds the call, with many the products.  32 / 8 heads of 128, one sequence of
+  // 32K keys / 32 of 2.5K on average, bf16: 32 rows take 39 / 94 us on the decode
+  // kernel and 53 / 99 on tcgen05, 64 rows 59 / 141 and 57 / 102.  fp32: 32 rows
+  // 209 / 369 us by warps and 243 / 559 by tiles, 64 rows 387 / 650 and 246 / 566.
+  const bool few = (int64_t)dm.tokens * dm.G <= 32 * (int64_t)dm.batch;
   if (dtype == MOBA_BF16)
     return few ? launch_paged_decode(dm, d, a, ws, stream, launches) : launch_paged_tc(dm, d, a, ws, stream, launches);
   if (!few) return launch_paged_f32(dm, d, a, ws, stream, launches);
