@@ -14,22 +14,22 @@ namespace moba {
 
 // ---- combine ---------------------------------------------------------------
 // Joins the cut items: weights 2^(m_i - m) of their parts' sums.  A unit is the
-// item that worker w begins and kRows of its rows, kShare warps a row that
-// divide the parts.  Units of one worker go to blocks apart, and a block looks
+// item that worker w begins and kRows of its rows.  Short row tiles may be in
+// hundreds of parts: kShare warps a row divide them.  Units of one worker go to blocks apart, and a block looks
 // at the headers of all its units at once: most are empty.  (One block an item,
 // its rows in turn, took 75 us to join 8 items of 74 parts and 80 us for items of
 // 256 rows.)
 // a prime number of blocks: the units of a worker, E apart, meet in none
 constexpr int kCombineGrid = 1181, kCombineThreads = 256;
 
-template <typename T, int D, int kShare>
+template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedHeader* __restrict__ hdr, int E, int BR,
                                                                         const float* __restrict__ part_o,
                                                                         const float* __restrict__ part_ml,
                                                                         T* __restrict__ out, float* __restrict__ lse,
                                                                         PagedDims dm) {
-  constexpr int C = D / 32, kWarps = kCombineThreads / 32, kRows = kWarps / kShare;
-  __shared__ float sm_o[kShare > 1 ? kWarps : 1][D];
+  constexpr int C = D / 32, kWarps = kCombineThreads / 32, kShare = 4, kRows = kWarps / kShare;
+  __shared__ float sm_o[kWarps][D];
   __shared__ float sm_l[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // launched while the attention kernel runs: what follows waits for its writes
@@ -69,21 +69,19 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
           }
         }
       }
-      if constexpr (kShare > 1) {
-        if (lane == 0) sm_l[warp] = l;
+      if (lane == 0) sm_l[warp] = l;
 #pragma unroll
-        for (int c = 0; c < C; ++c) sm_o[warp][lane * C + c] = o[c];
-        __syncthreads();
-        if (warp % kShare == 0) {
+      for (int c = 0; c < C; ++c) sm_o[warp][lane * C + c] = o[c];
+      __syncthreads();
+      if (warp % kShare == 0) {
 #pragma unroll
-          for (int i = 1; i < kShare; ++i) {
-            l += sm_l[warp + i];
+        for (int i = 1; i < kShare; ++i) {
+          l += sm_l[warp + i];
 #pragma unroll
-            for (int c = 0; c < C; ++c) o[c] += sm_o[warp + i][lane * C + c];
-          }
+          for (int c = 0; c < C; ++c) o[c] += sm_o[warp + i][lane * C + c];
         }
-        __syncthreads();
       }
+      __syncthreads();
       if (on && warp % kShare == 0) {
         const int row = h.row0 + r, tok = row / dm.G, head = h.h * dm.G + row % dm.G;
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -100,6 +98,68 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
         if (lane == 0 && lse != nullptr)
           lse[(size_t)head * dm.tokens + h.first + tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
+    }
+  }
+}
+
+// The same for long row tiles (in few parts): 8 lanes a row, 4 rows a warp.  (A
+// warp a row spent 20 us on its own instructions for 148 items of 256 rows.)
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_rows_kernel(const PagedHeader* __restrict__ hdr, int E,
+                                                                             int BR, const float* __restrict__ part_o,
+                                                                             const float* __restrict__ part_ml,
+                                                                             T* __restrict__ out, float* __restrict__ lse,
+                                                                             PagedDims dm) {
+  constexpr int V = D / 32, kRows = kCombineThreads / 8;   // groups of 4 channels a lane, rows a unit
+  const int lane = threadIdx.x & 31, sub = threadIdx.x & 7;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int units = E * (BR / kRows);
+  for (int u0 = blockIdx.x; u0 < units; u0 += 32 * gridDim.x) {
+    const int mine = u0 + lane * gridDim.x;
+    const int parts = mine < units ? hdr[mine % E].parts : 0;
+    for (uint32_t live = __ballot_sync(0xffffffffu, parts > 0); live != 0; live &= live - 1) {
+      const int u = u0 + (__ffs(live) - 1) * gridDim.x, w = u % E;
+      const PagedHeader h = hdr[w];
+      if (u / E * kRows >= h.rows) continue;
+      const int r = u / E * kRows + (threadIdx.x >> 3);
+      const bool on = r < h.rows;
+      // part 0 is slot 2w + 1, part i > 0 is slot 2(w + i)
+      const size_t at0 = (size_t)(2 * w + 1) * BR + (on ? r : 0), step = (size_t)2 * BR;
+      auto slot = [&](int i) { return i == 0 ? at0 : at0 - BR + i * step; };
+      float m = -INFINITY, l = 0.f;
+      for (int i = sub; i < h.parts; i += 8) m = fmaxf(m, part_ml[2 * slot(i)]);
+#pragma unroll
+      for (int x = 4; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const float mb = m == -INFINITY ? 0.f : m;
+      float4 o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < h.parts; ++i) {
+        const size_t sl = slot(i);
+        const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * sl);
+        const float wt = exp2f(ml.x - mb);
+        l = fmaf(ml.y, wt, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float4 x = *reinterpret_cast<const float4*>(part_o + sl * D + 32 * v + 4 * sub);
+          o[v] = make_float4(fmaf(x.x, wt, o[v].x), fmaf(x.y, wt, o[v].y), fmaf(x.z, wt, o[v].z), fmaf(x.w, wt, o[v].w));
+        }
+      }
+      if (!on) continue;
+      const int row = h.row0 + r, tok = row / dm.G, head = h.h * dm.G + row - tok * dm.G;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* dst = out + ((size_t)(h.first + tok) * dm.hq + head) * D + 4 * sub;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(dst + 32 * v) = make_float4(o[v].x * inv, o[v].y * inv, o[v].z * inv, o[v].w * inv);
+        else
+          *reinterpret_cast<uint2*>(dst + 32 * v) =
+              make_uint2(pack_bf16x2(o[v].x * inv, o[v].y * inv), pack_bf16x2(o[v].z * inv, o[v].w * inv));
+      }
+      if (sub == 0 && lse != nullptr)
+        lse[(size_t)head * dm.tokens + h.first + tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
 }
@@ -385,7 +445,7 @@ cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int 
     c.attrs = &at;
     c.numAttrs = 1;
     // long row tiles are in few parts, short ones may be in hundreds
-    auto* kernel = BR > 16 ? paged_combine_kernel<T, decltype(dim)::value, 1> : paged_combine_kernel<T, decltype(dim)::value, 4>;
+    auto* kernel = BR > 16 ? paged_combine_rows_kernel<T, decltype(dim)::value> : paged_combine_kernel<T, decltype(dim)::value>;
     return cudaLaunchKernelEx(&c, kernel, (const PagedHeader*)l.hdr, E, BR, (const float*)l.part_o, (const float*)l.part_ml,
                               out, a.lse, dm);
   };
