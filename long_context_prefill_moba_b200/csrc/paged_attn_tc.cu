@@ -208,8 +208,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (int b = tid; b < dm.batch; b += kThreads)
       if (a.kv_len[b] > ((int64_t)dm.max_pages << dm.page_shift)) atomicExch(a.status, (int)MOBA_ERR_INTERNAL);
   if (me >= E) return;
-  paged_rounds<kBR, kBK, kItemCost>(rounds, plan, W, E, a.cu, a.kv_len, dm);
-  const Line line{plan, rounds, a, dm, E, me};
 
   if (tid == 0) {
     for (int w = 0; w < 2; ++w) {
@@ -237,7 +235,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  paged_rounds<kBR, kBK, kItemCost>(rounds, plan, W, E, a.cu, a.kv_len, dm);   // ends with a block barrier
+  const Line line{plan, rounds, a, dm, E, me};
   tc_fence_after();
   const uint32_t tb = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
