@@ -97,19 +97,32 @@ MOBA_DEV int64_t block_prefix(int64_t v, int64_t (&warp_sum)[NT / 32], int64_t& 
   return base + inc - v;
 }
 
-// Whole block of NT threads: fills the plan, returns W.
+// Whole block of NT threads: fills the plan, returns W.  `items` (where wanted): the
+// items before the sequences of each thread, and the largest item's tiles.
 template <int BR, int BK, int X, int NT>
 MOBA_DEV int64_t paged_plan(PagedPlan<NT>& p, const int32_t* __restrict__ cu, const int32_t* __restrict__ kv_len,
-                            const PagedDims& dm) {
+                            const PagedDims& dm, int64_t* items = nullptr, int* largest = nullptr) {
   const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
-  int64_t w = 0;
+  int64_t w = 0, n = 0, sum;
+  int most = 1;
   for (int i = 0; i < per; ++i) {
     const int b = t * per + i;
     PagedSeq x = {0, 0, 0};
     if (b < dm.batch) x = paged_seq(cu, kv_len, dm, b);
     w += paged_head_tiles<BR, BK, X>(x, dm.G) * dm.hkv;
+    if (items != nullptr && x.n > 0) {
+      const int nrt = paged_row_tiles<BR>(x, dm.G);
+      n += (int64_t)nrt * dm.hkv;
+      most = max(most, paged_tiles<BR, BK, X>(x, dm.G, nrt - 1));
+    }
   }
-  int64_t sum;
+  if (items != nullptr) {
+    if (t == 0) *largest = 1;
+    most = __reduce_max_sync(0xffffffffu, most);
+    int64_t all;
+    items[t] = block_prefix<NT>(n, p.warp_sum, all);   // its barriers order the line above before the maxima
+    if ((t & 31) == 0) atomicMax(largest, most);
+  }
   p.before[t] = block_prefix<NT>(w, p.warp_sum, sum);
   if (t == 0) p.before[NT] = sum;
   __syncthreads();
@@ -225,33 +238,25 @@ MOBA_DEV PagedItem paged_locate_item(const PagedRounds<NT, MAXE>& r, int64_t at,
   return it;
 }
 
-// Whole block, after paged_plan.
+// Whole block, after paged_plan has filled r.items and r.largest.  Ends with a block barrier.
 template <int BR, int BK, int X, int NT, int MAXE>
 MOBA_DEV void paged_rounds(PagedRounds<NT, MAXE>& r, PagedPlan<NT>& p, int64_t W, int E, const int32_t* __restrict__ cu,
                            const int32_t* __restrict__ kv_len, const PagedDims& dm) {
-  const int per = (dm.batch + NT - 1) / NT, t = threadIdx.x;
-  if (t == 0) r.largest = 1;
-  for (int i = t; i < MAXE; i += NT) r.whole[i] = 0;
-  __syncthreads();
-  int64_t n = 0, sum;
-  int largest = 0;
-  for (int b = t * per; b < min((t + 1) * per, dm.batch); ++b) {
-    const PagedSeq s = paged_seq(cu, kv_len, dm, b);
-    const int nrt = paged_row_tiles<BR>(s, dm.G);
-    n += (int64_t)nrt * dm.hkv;
-    if (nrt > 0) largest = max(largest, paged_tiles<BR, BK, X>(s, dm.G, nrt - 1));
+  const int t = threadIdx.x, rounds = (int)((W / E - 1) / r.largest);
+  int64_t before = 0, sum = 0;   // tiles in whole items: of the workers before this thread's, and of all
+  if (rounds > 0) {
+    for (int i = t; i < MAXE; i += NT) r.whole[i] = 0;
+    __syncthreads();
+    for (int64_t i = t; i < (int64_t)rounds * E; i += NT)
+      atomicAdd(&r.whole[i % E], (unsigned long long)paged_locate_item<BR, BK, X>(r, i, cu, kv_len, dm).tiles);
+    __syncthreads();
+    before = block_prefix<NT>(t < E ? (int64_t)r.whole[t] : 0, p.warp_sum, sum);
   }
-  if (largest > 0) atomicMax(&r.largest, largest);
-  r.items[t] = block_prefix<NT>(n, p.warp_sum, sum);
-  if (t == 0) r.rounds = (int)((W / E - 1) / r.largest);
-  __syncthreads();
-  for (int64_t i = t; i < (int64_t)r.rounds * E; i += NT)
-    atomicAdd(&r.whole[i % E], (unsigned long long)paged_locate_item<BR, BK, X>(r, i, cu, kv_len, dm).tiles);
-  __syncthreads();
-  const int64_t mine = t < E ? (int64_t)r.whole[t] : 0;
-  const int64_t before = block_prefix<NT>(mine, p.warp_sum, sum);   // sum: the line up to the rest
   if (t < E) r.start[t] = sum + t * W / E - before;
-  if (t == 0) r.start[E] = W;
+  if (t == 0) {
+    r.start[E] = W;
+    r.rounds = rounds;
+  }
   __syncthreads();
 }
 

@@ -211,7 +211,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::);
-  const int64_t W = paged_plan<kBR, kBK, kItemCost, kThreads>(plan, a.cu, a.kv_len, dm);
+  const int64_t W = paged_plan<kBR, kBK, kItemCost, kThreads>(plan, a.cu, a.kv_len, dm, rounds.items, &rounds.largest);
   const int E = (int)min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles), me = blockIdx.x;
   if (tid == 0) hdr[me].parts = 0;
   if (blockIdx.x == 0 && a.status != nullptr)
@@ -466,18 +466,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               a.lse[(size_t)head * dm.tokens + p.first + tok] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
           } else {
             const size_t slot = (size_t)(begins ? 2 * me + 1 : 2 * me) * kBR + w * kQT + rho;
+            const uint32_t stg = base + Gm::kOffOut + (uint32_t)warp * Gm::kOutWarp;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t o[32];
               tmem_ld32(tO + cc * 32, o);
               tmem_wait_ld();
               if (some) add_bad(o, cc);
-              if (valid) {
-                float4* dst = reinterpret_cast<float4*>(part_o + slot * D + cc * 32);
+              // 16 channels of the warp's 32 rows at a time, so that a store writes 64 bytes of 8 rows
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+              for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  st_shared_v4(stg + stage_off(lane, e), o[16 * hh + 4 * e], o[16 * hh + 4 * e + 1], o[16 * hh + 4 * e + 2],
+                               o[16 * hh + 4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int k2 = 0; k2 < 4; ++k2) {
+                  const int rl = 8 * k2 + (lane >> 2);
+                  const uint4 x = ld_shared_v4(stg + stage_off(rl, lane & 3));
+                  if (w * kQT + (warp & 3) * 32 + rl < p.rows)
+                    *reinterpret_cast<uint4*>(part_o + (slot - lane + rl) * D + cc * 32 + hh * 16 + (lane & 3) * 4) = x;
+                }
+                __syncwarp();
               }
             }
             if (valid) *reinterpret_cast<float2*>(part_ml + 2 * slot) = make_float2(m_used, l);
