@@ -30,8 +30,8 @@
 // before P(i), which lies in its place, is read.  Measured (32 / 8 heads of 128):
 // 4096 tokens at 131072 in 7.7 ms, 1120 TFLOP/s (0.81 of the library product's
 // sustained rate, both under the power cap), 2048 at 65536 in 1.84 ms (1177); a
-// prompt of 8192 tokens 590 us (930), of 2048 80 us (430), where setting up (7 us),
-// queries, mask and epilogue of each item (some 6 us) and the joining of cut items
+// prompt of 8192 tokens 544 us (1010), of 2048 75 us (457), where setting up (6 us),
+// queries, mask and epilogue of each item (some 5 us) and the joining of cut items
 // (8 us) count.  At D = 64 the MMAs take half, the exponentials the same: 490
 // TFLOP/s.
 //
@@ -55,11 +55,12 @@ using namespace sm100;
 constexpr int kQT = 128, kBK = 128, kBR = 256;
 constexpr int kThreads = 384;
 constexpr int kWorkers = 148;            // one CTA an SM
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;
 // What an item costs beside its tiles (2.1 us each): its queries' load, the
-// cleaning at the mask and the epilogue take some 6 us.  With no cost counted,
+// cleaning at the mask and the epilogue take some 5 us.  With no cost counted,
 // the workers of a short prompt's first items ended after 92 us and those of its
-// last after 50.
+// last after 50.  1, 2, 3, 4, 5 tiles: 79, 78, 75, 75, 75 us for 2048 tokens, 588,
+// 558, 544, 547, 553 for 8192.
 constexpr int kItemCost = 3;
 constexpr int kReaders = 11;             // warps 0-10 read the planner's parts
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 64;
