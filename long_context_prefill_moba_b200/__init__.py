@@ -653,133 +653,27 @@ def moba_rope_inv_freq(rot_dim, theta=10000.0, device="cuda"):
     return theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
 
 
-def _require(ok, where, what):
-    if not ok:
-        raise ValueError(f"{where}: {what}")
+_binding = None
 
 
-def _row_step(x, where, name):
-    """The elements between the tokens of x [..., h, d] where its rows lie one stride
-    apart (part of a fused projection); None where they do not (a dense copy is used)."""
-    _require(x.dim() >= 3 and x.is_cuda, where, f"{name} must be a CUDA tensor [..., heads, head_dim]")
-    h, d = x.shape[-2:]
-    st = x.stride()
-    step = st[-3]
-    if (st[-1] == 1 and (h == 1 or st[-2] == d) and step >= h * d and step * x.element_size() % 16 == 0
-            and all(x.shape[i] == 1 or st[i] == st[i + 1] * x.shape[i + 1] for i in range(x.dim() - 3))):
-        return step
-    return None
-
-
-def _same(where, ref, dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _require(t.dtype == dtype and t.device == ref.device, where,
-                     f"{name} must be {dtype} on {ref.device}, not {t.dtype} on {t.device}")
-
-
-def _dense(where, **tensors):
-    for name, t in tensors.items():
-        _require(t is None or t.is_contiguous(), where, f"{name} must be contiguous")
-
-
-# What a call's shapes, strides and types decide (its checked shape structure, its
-# workspace) is worked out once for each signature: the checks cost several times
-# the launch of a small step.
-_plans: dict = {}
-
-
-def _sig(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
-
-
-def _plan(key, make, *args):
-    p = _plans.get(key)
-    if p is None:
-        p = make(*args)
-        if len(_plans) >= 1024:
-            _plans.clear()
-        _plans[key] = p
-    return p
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
-
-
-def _enqueue(device, where, fn, *args):
-    """fn(*args, stream) on the device's current stream, the device being current."""
-    if torch.cuda.current_device() == device:
-        status = fn(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device))
-    if status != MOBA_OK:
-        raise MobaError(status, where)
-
-
-class _NormRopePlan:
-    def __init__(self, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
-        where = "moba_norm_rope"
-        qs, ks = _row_step(q, where, "q"), _row_step(k, where, "k")
-        _require(q.dtype in _DTYPES and q_weight.dtype in _DTYPES, where, "bf16 or fp32 tensors")
-        _same(where, q, q.dtype, k=k)
-        _same(where, q, q_weight.dtype, q_weight=q_weight, k_weight=k_weight)
-        _same(where, q, torch.int32, positions=positions)
-        _same(where, q, torch.float64, inv_freq=inv_freq)
-        _dense(where, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
-        hq, d = q.shape[-2:]
-        hkv = k.shape[-2]
-        _require(k.shape[:-2] == q.shape[:-2] and k.shape[-1] == d, where, "q and k must hold the same tokens and head_dim")
-        _require(q_weight.shape == (d,) and k_weight.shape == (d,), where, "the weights must be [head_dim]")
-        tokens = math.prod(q.shape[:-2])
-        _require(positions.numel() == tokens, where, "one position a token")
-        self.copy_q, self.copy_k = qs is None, ks is None
-        self.shape = make_rope_shape(tokens, hq, hkv, d, 2 * inv_freq.numel(), q.dtype, q_weight.dtype, eps, interleaved,
-                                     qs or 0, ks or 0)
-        _check(moba_check_rope_shape(self.shape), where)
-        self.ref = ctypes.byref(self.shape)
-        self.ws_bytes = moba_qk_norm_rope_bwd_workspace_size(self.shape)
-        self.device = q.get_device()
-
-
-def _norm_rope_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
-    key = ("norm_rope", eps, interleaved, _sig(q), _sig(k), _sig(q_weight), _sig(k_weight), _sig(positions), _sig(inv_freq))
-    p = _plan(key, _NormRopePlan, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-    if p.copy_q:
-        q = q.contiguous()
-    if p.copy_k:
-        k = k.contiguous()
-    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
-    _enqueue(p.device, "moba_norm_rope", _lib.moba_qk_norm_rope, p.ref, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-             k_weight.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(), k_out.data_ptr())
-    return p, q, k, q_out, k_out
-
-
-class _MobaNormRope(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
-        ctx.plan, q, k, q_out, k_out = _norm_rope_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-        return q_out, k_out
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dq_out, dk_out):
-        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
-        p = ctx.plan
-        dq_out, dk_out = dq_out.contiguous(), dk_out.contiguous()
-        dq, dk, dqw, dkw = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q_weight), torch.empty_like(k_weight)
-        ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=q.device)
-        _enqueue(p.device, "moba_norm_rope", _lib.moba_qk_norm_rope_bwd, p.ref, q.data_ptr(), k.data_ptr(),
-                 q_weight.data_ptr(), k_weight.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), dq_out.data_ptr(),
-                 dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws.data_ptr(), p.ws_bytes)
-        return dq, dk, dqw, dkw, None, None, None, None
+def load_binding():
+    """The torch extension behind the three calls below: checks, outputs, workspace and
+    the C calls in one native step (raises if it is missing)."""
+    global _binding
+    if _binding is None:
+        path = os.path.join(HERE, "_moba_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m long_context_prefill_moba_b200.build` (no CPU fallback exists)")
+        lib()
+        from . import _moba_torch
+        _binding = _moba_torch
+    return _binding
 
 
 def moba_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False):
     """Norm of every query and key head and the position rotation, in one pass and
-    differentiable in q, k and the weights: what precedes moba_attention in a layer.
+    differentiable (once) in q, k and the weights: what precedes moba_attention in a layer.
 
     q [..., Hq, d], k [..., Hkv, d] with the same leading dimensions (rows of a fused
     projection are read where they lie), q_weight/k_weight [d], positions int32 with
@@ -787,61 +681,7 @@ def moba_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, inte
     (q_out, k_out), dense.  Runs on the current stream of q's device.  A step captured
     into a CUDA graph with its backward needs every earlier autograd graph of the same
     leaves freed first (torch ties a leaf's gradient node to the stream it was made on)."""
-    lib()
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or q_weight.requires_grad or k_weight.requires_grad):
-        return _MobaNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-    return _norm_rope_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)[3:]
-
-
-def _paged_shape(where, ref, hq, k_pool, v_pool, cu_new, kv_len, table, status, tokens, scale=None, strides=(0, 0, 0)):
-    _require(k_pool.dim() == 4 and k_pool.shape == v_pool.shape, where,
-             "the pools must be [num_pages, heads, page_size, head_dim], alike")
-    pages, hkv, page, d = k_pool.shape
-    _require(ref.dtype in _DTYPES, where, "bf16 or fp32 tensors")
-    for name, p in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _require(p.stride()[1:] == (page * d, d, 1), where, f"a page of {name} must be dense")
-    _same(where, ref, ref.dtype, k_pool=k_pool, v_pool=v_pool)
-    _same(where, ref, torch.int32, cu_new=cu_new, kv_len=kv_len, table=table, status=status)
-    _dense(where, cu_new=cu_new, kv_len=kv_len, table=table, status=status)
-    _require(status is None or status.numel() == 1, where, "status must be one int32")
-    _require(table.dim() == 2 and kv_len.shape == (table.shape[0],) and cu_new.shape == (table.shape[0] + 1,), where,
-             "table must be [batch, max_pages], kv_len [batch], cu_new [batch + 1]")
-    _require(ref.shape[-1] == d and hq % hkv == 0, where, "the heads must match the pools'")
-    shape = make_paged_shape(table.shape[0], tokens, hq, hkv, d, page, pages, table.shape[1], ref.dtype, scale, *strides,
-                             k_pool.stride(0) if pages > 1 else 0, v_pool.stride(0) if pages > 1 else 0)
-    _check(moba_check_paged_shape(shape), where)
-    return shape
-
-
-class _AppendPlan:
-    def __init__(self, k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq, q, q_weight, k_weight, eps, interleaved, status,
-                 q_out):
-        where = "moba_cache_append"
-        ks, vs = _row_step(k, where, "k"), _row_step(v, where, "v")
-        _require(k.dim() == 3 and k.shape == v.shape and k.shape[1:] == k_pool.shape[1::2], where,
-                 "k and v must be [tokens, heads, head_dim] with the pools' heads")
-        _same(where, k, k.dtype, v=v, q=q, q_out=q_out)
-        qs = None
-        if q is not None:
-            qs = _row_step(q, where, "q")
-            _require(q.dim() == 3 and q.shape[0] == k.shape[0], where, "q must hold the same tokens as k")
-            _require(q_out is None or q_out.shape == q.shape, where, "q_out must have q's shape")
-        _require(q is not None or (q_weight is None and q_out is None), where, "q_weight and q_out go with q")
-        weight = q_weight if q_weight is not None else k_weight
-        _require(weight is None or weight.dtype in _DTYPES, where, "bf16 or fp32 weights")
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                _same(where, k, weight.dtype, **{name: w})
-                _require(w.shape == k.shape[-1:], where, "the weights must be [head_dim]")
-        _same(where, k, torch.float64, inv_freq=inv_freq)
-        _dense(where, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, q_out=q_out)
-        self.copy_q, self.copy_k, self.copy_v = q is not None and qs is None, ks is None, vs is None
-        self.shape = _paged_shape(where, k, k.shape[1] if q is None else q.shape[1], k_pool, v_pool, cu_new, kv_len, table,
-                                  status, k.shape[0], None, (qs or 0, ks or 0, vs or 0))
-        self.rope = MobaRope(0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
-                             MOBA_BF16 if weight is None else _DTYPES[weight.dtype], eps)
-        self.refs = ctypes.byref(self.shape), ctypes.byref(self.rope)
-        self.device = k.get_device()
+    return (_binding or load_binding()).norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
 
 
 def moba_cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq=None, q=None, q_weight=None,
@@ -855,40 +695,8 @@ def moba_cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq=None
     zeroed int32 CUDA tensor that becomes nonzero if a token had no page.  Returns the
     queries (None without q): q_out, or a new tensor whose rows from cu_new[-1] on
     are not written.  Runs on the current stream of k's device."""
-    L = lib()
-    key = ("append", eps, interleaved, _sig(k), _sig(v), _sig(cu_new), _sig(kv_len), _sig(table), _sig(k_pool), _sig(v_pool),
-           _sig(inv_freq), _sig(q), _sig(q_weight), _sig(k_weight), _sig(status), _sig(q_out))
-    p = _plan(key, _AppendPlan, k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq, q, q_weight, k_weight, eps, interleaved,
-              status, q_out)
-    if p.copy_k:
-        k = k.contiguous()
-    if p.copy_v:
-        v = v.contiguous()
-    if q is not None:
-        if p.copy_q:
-            q = q.contiguous()
-        if q_out is None:
-            q_out = torch.empty_like(q)
-    _enqueue(p.device, "moba_cache_append", L.moba_paged_append, *p.refs, _at(q), k.data_ptr(), v.data_ptr(), _at(q_weight),
-             _at(k_weight), _at(inv_freq), cu_new.data_ptr(), kv_len.data_ptr(), table.data_ptr(), _at(q_out),
-             k_pool.data_ptr(), v_pool.data_ptr(), _at(status))
-    return q_out
-
-
-class _AttendPlan:
-    def __init__(self, q, k_pool, v_pool, cu_new, kv_len, table, scale, out, status):
-        where = "moba_cache_attention"
-        qs = _row_step(q, where, "q")
-        _require(q.dim() == 3, where, "q must be [tokens, heads, head_dim]")
-        self.copy_q = qs is None
-        self.shape = _paged_shape(where, q, q.shape[1], k_pool, v_pool, cu_new, kv_len, table, status, q.shape[0], scale,
-                                  (qs or 0, 0, 0))
-        _same(where, q, q.dtype, out=out)
-        _dense(where, out=out)
-        _require(out is None or out.shape == q.shape, where, "out must have q's shape")
-        self.ref = ctypes.byref(self.shape)
-        self.ws_bytes = moba_paged_attn_workspace_size(self.shape)
-        self.device = q.get_device()
+    return (_binding or load_binding()).cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq, q, q_weight,
+                                                     k_weight, eps, interleaved, status, q_out)
 
 
 def moba_cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale=None, return_lse=False, out=None, status=None):
@@ -901,17 +709,6 @@ def moba_cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale=None, r
     not written.  The workspace comes from torch's allocator, so that calls on
     several streams, and captured graphs, have one each.  Runs on the current stream
     of q's device."""
-    L = lib()
-    key = ("attend", scale, _sig(q), _sig(k_pool), _sig(v_pool), _sig(cu_new), _sig(kv_len), _sig(table), _sig(out),
-           _sig(status))
-    p = _plan(key, _AttendPlan, q, k_pool, v_pool, cu_new, kv_len, table, scale, out, status)
-    if p.copy_q:
-        q = q.contiguous()
-    if out is None:
-        out = torch.empty_like(q)
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if return_lse else None
-    ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=q.device)
-    _enqueue(p.device, "moba_cache_attention", L.moba_paged_attn, p.ref, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-             cu_new.data_ptr(), kv_len.data_ptr(), table.data_ptr(), out.data_ptr(), _at(lse), _at(status), ws.data_ptr(),
-             p.ws_bytes)
+    out, lse = (_binding or load_binding()).cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale, return_lse, out,
+                                                            status)
     return (out, lse) if return_lse else out

@@ -209,6 +209,20 @@ def test_layouts_that_are_copied(cuda_device):
         assert (one[0] == 0).all() and torch.isfinite(one[1]).all()
 
 
+def test_second_derivatives_are_refused(cuda_device):
+    import long_context_prefill_moba_b200 as M
+    dev = cuda_device
+    leaves = [torch.randn(3, 2, 64, device=dev).requires_grad_(), torch.randn(3, 1, 64, device=dev).requires_grad_(),
+              torch.ones(64, device=dev), torch.ones(64, device=dev)]
+    out = M.moba_norm_rope(*leaves, torch.arange(3, dtype=torch.int32, device=dev), M.moba_rope_inv_freq(64, device=dev))
+    with pytest.raises(RuntimeError, match="not differentiable"):
+        torch.autograd.grad(out[0].sum(), leaves[0], create_graph=True)
+    # only some of the leaves need gradients, or one output is used
+    g = torch.autograd.grad(M.moba_norm_rope(*leaves, torch.arange(3, dtype=torch.int32, device=dev),
+                                             M.moba_rope_inv_freq(64, device=dev))[1].square().sum(), leaves[:2])
+    assert (g[0] == 0).all() and g[1].abs().max() > 0
+
+
 def test_no_tokens(cuda_device):
     import long_context_prefill_moba_b200 as M
     dev = cuda_device

@@ -156,6 +156,15 @@ def test_binding_refuses_cpu_tensors():
         M.moba_cache_attention(t, torch.zeros(2, 4, 16, 64), torch.zeros(2, 4, 16, 64), i, i[:1], i[None])
 
 
+def test_binding_is_built_beside_the_library(L):
+    import os
+    path = B.build_binding()
+    assert os.path.dirname(path) == os.path.dirname(B.LIB) and os.path.exists(path)
+    assert M.load_binding() is M.load_binding()
+    for name in ("norm_rope", "cache_append", "cache_attention"):
+        assert callable(getattr(M.load_binding(), name))
+
+
 def test_inv_freq():
     f = M.moba_rope_inv_freq(64, 10000.0, "cpu")
     assert f.dtype == torch.float64 and f.shape == (32,) and f[0] == 1.0 and abs(f[16] - 0.01) < 1e-15
