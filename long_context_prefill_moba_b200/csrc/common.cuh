@@ -82,6 +82,12 @@ MOBA_DEV void cp_async16(uint32_t dst, const void* src, bool pred) {
 MOBA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
 template <int N> MOBA_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N)); }
 
+// ---- kernels that overlap the end of the one before (launch_early) -----------
+MOBA_DEV void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
 // slot of block j in a sorted selection list (entries < j that are valid)
 MOBA_DEV int slot_of(const int32_t* sel_row, int topk, int j) {
   int s = 0;

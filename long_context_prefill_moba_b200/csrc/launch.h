@@ -116,6 +116,24 @@ cudaError_t launch_index_check(const Dims& dm, int exact, int32_t* sel, int32_t*
                                const int32_t* rows, int64_t capacity, int* status, cudaStream_t stream,
                                int* launches);
 
+// Launch that may begin while the kernel before it in the stream ends: the kernel
+// waits (after_previous) before it touches global memory, and lets its own
+// successor begin once all of its blocks run.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // per-head norm and position rotation (norm_rope.cu).  The backward reads q, k
 // (the forward's inputs) and writes the gradients to q_out, k_out.
 struct RopeArgs {

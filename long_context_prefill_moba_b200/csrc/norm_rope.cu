@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(R
   __shared__ Angles<LPH> cs_all[kWarps];
   __shared__ float sums[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::);   // the reduction kernel may be launched
   const bool isq = (int)blockIdx.x < nbq;
   const int nb = isq ? nbq : gridDim.x - nbq, bi = isq ? blockIdx.x : blockIdx.x - nbq;
   const int heads = isq ? a.hq : a.hkv, groups = (heads + HPW - 1) / HPW;
@@ -482,16 +482,17 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(R
   }
 }
 
-// dw of the queries (blocks y = 0) and of the keys (y = 1): 32 channels a block,
+// dw of the queries (the first D / 32 blocks) and of the keys: 32 channels a block,
 // whose 32 warps add the rows of `part`, in a fixed order.  (One block for all
 // channels took 10 us for 592 rows.)
 template <int D>
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int nbq, int nbk,
                                                             void* dqw, void* dkw, int weight_f32) {
   __shared__ float sums[32][33];
-  const int lane = threadIdx.x & 31, p = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // launched while the backward kernel runs
-  const int lo = blockIdx.y == 0 ? 0 : nbq, hi = blockIdx.y == 0 ? nbq : nbq + nbk;
+  const int lane = threadIdx.x & 31, p = threadIdx.x >> 5, slab = blockIdx.x % (D / 32), c = slab * 32 + lane;
+  const bool isq = blockIdx.x < D / 32;
+  after_previous();
+  const int lo = isq ? 0 : nbq, hi = isq ? nbq : nbq + nbk;
   float v = 0.f;
 #pragma unroll 8
   for (int i = lo + p; i < hi; i += 32) v += part[(int64_t)i * D + c];
@@ -499,8 +500,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
   __syncthreads();
   v = warp_sum(sums[lane][p]);   // channel p of the block
   if (lane == 0) {
-    void* dst = blockIdx.y == 0 ? dqw : dkw;
-    const int at = blockIdx.x * 32 + p;
+    void* dst = isq ? dqw : dkw;
+    const int at = slab * 32 + p;
     if (weight_f32) ((float*)dst)[at] = v; else ((__nv_bfloat16*)dst)[at] = __float2bfloat16_rn(v);
   }
 }
@@ -514,6 +515,7 @@ cudaError_t launch_fwd(RopeArgs a, bool append, cudaStream_t stream, int* launch
   const int64_t need = ((int64_t)a.tokens * a.split + kWarps - 1) / kWarps;
   const int64_t blocks = need < kFwdBlocks<T> * kSms ? need : kFwdBlocks<T> * kSms;
   if (blocks == 0) return cudaSuccess;
+  // (launched early like the attention's kernels it gained nothing: 75 us for chunks became 78)
   if (append)
     norm_rope_kernel<T, D, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   else
@@ -545,19 +547,11 @@ cudaError_t launch_bwd(const RopeArgs& a, const void* dq_out, const void* dk_out
   if (nbq + nbk > 0) {
     norm_rope_bwd_kernel<T, D><<<nbq + nbk, kThreads, 0, stream>>>(a, dq_out, dk_out, part, nbq);
     ++*launches;
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(D / 32, 2);
-  c.blockDim = dim3(1024);
-  c.stream = stream;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, norm_rope_dw_kernel<D>, (const float*)part, nbq, nbk, dqw, dkw, a.weight_f32);
+  // D / 32 blocks for the queries and as many for the keys
+  const cudaError_t e = launch_early(norm_rope_dw_kernel<D>, 2 * (D / 32), 1024, 0, stream, part, nbq, nbk, dqw, dkw, a.weight_f32);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   __shared__ float sm_o[kWarps][D];
   __shared__ float sm_l[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // launched while the attention kernel runs: what follows waits for its writes
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  after_previous();
   const int units = E * ((BR + kRows - 1) / kRows);
   for (int u0 = blockIdx.x; u0 < units; u0 += 32 * gridDim.x) {
     const int mine = u0 + lane * gridDim.x;
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_rows_kernel(con
                                                                              PagedDims dm) {
   constexpr int V = D / 32, kRows = kCombineThreads / 8;   // groups of 4 channels a lane, rows a unit
   const int lane = threadIdx.x & 31, sub = threadIdx.x & 7;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  after_previous();
   const int units = E * (BR / kRows);
   for (int u0 = blockIdx.x; u0 < units; u0 += 32 * gridDim.x) {
     const int mine = u0 + lane * gridDim.x;
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(kVecThreads, vec_blocks(R)) paged_vec_kernel(P
   __shared__ __align__(16) float sp[kVecWarps][N];
   __shared__ float sa[kVecWarps][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  after_previous();
   const int64_t W = paged_plan<R, kVecBK, 0, kVecThreads>(plan, a.cu, a.kv_len, dm);
   const int64_t E = min((int64_t)vec_workers(R), (W + kVecMinTiles - 1) / kVecMinTiles);
   const int64_t w = (int64_t)blockIdx.x * kVecWarps + warp;
@@ -413,10 +412,10 @@ template <typename T, int D, int R>
 cudaError_t launch_vec(const PagedDims& dm, const PagedArgs& a, void* ws, cudaStream_t stream, int* launches) {
   constexpr int kE = vec_workers(R);
   const PagedWs l = paged_ws_layout(ws, kE, R);
-  paged_vec_kernel<T, D, R><<<kE / kVecWarps, kVecThreads, 0, stream>>>(a, dm, l.hdr, l.part_o, l.part_ml);
-  ++*launches;
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(paged_vec_kernel<T, D, R>, kE / kVecWarps, kVecThreads, 0, stream, a, dm, l.hdr, l.part_o,
+                               l.part_ml);
   if (e != cudaSuccess) return e;
+  ++*launches;
   return launch_paged_combine(sizeof(T) == 2 ? MOBA_BF16 : MOBA_F32, D, l, kE, R, a, dm, stream, launches);
 }
 
@@ -437,19 +436,9 @@ cudaError_t launch_paged_combine(int dtype, int d, const PagedWs& l, int E, int 
                                  cudaStream_t stream, int* launches) {
   auto go = [&](auto* out, auto dim) {
     using T = typename std::remove_pointer<decltype(out)>::type;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(kCombineGrid);
-    c.blockDim = dim3(kCombineThreads);
-    c.stream = stream;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    // long row tiles are in few parts, short ones may be in hundreds
     auto* kernel = BR > 16 ? paged_combine_rows_kernel<T, decltype(dim)::value> : paged_combine_kernel<T, decltype(dim)::value>;
-    return cudaLaunchKernelEx(&c, kernel, (const PagedHeader*)l.hdr, E, BR, (const float*)l.part_o, (const float*)l.part_ml,
-                              out, a.lse, dm);
+    return launch_early(kernel, kCombineGrid, kCombineThreads, 0, stream, (const PagedHeader*)l.hdr, E, BR,
+                        (const float*)l.part_o, (const float*)l.part_ml, out, a.lse, dm);
   };
   cudaError_t e;
   using D64 = std::integral_constant<int, 64>;

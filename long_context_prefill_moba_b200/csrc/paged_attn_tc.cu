@@ -211,7 +211,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   __shared__ Rounds rounds;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  after_previous();
   const int64_t W = paged_plan<kBR, kBK, kItemCost, kThreads>(plan, a.cu, a.kv_len, dm, rounds.items, &rounds.largest);
   const int E = (int)min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles), me = blockIdx.x;
   if (tid == 0) hdr[me].parts = 0;
@@ -778,8 +778,8 @@ cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cu
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<kWorkers, kThreads, Geo<D>::kSmem, stream>>>(mk, mv, a, dm, box, l.hdr, l.part_o, l.part_ml);
-  return cudaGetLastError();
+  return launch_early(paged_tc_kernel<D>, kWorkers, kThreads, Geo<D>::kSmem, stream, mk, mv, a, dm, box, l.hdr, l.part_o,
+                      l.part_ml);
 }
 
 }  // namespace

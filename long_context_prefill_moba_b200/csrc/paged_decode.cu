@@ -89,7 +89,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   __shared__ uint64_t full[kPairs][kStages], empty[kPairs][kStages];
   __shared__ int abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp & (kPairs - 1);
-  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  after_previous();
   if (tid < kPairs * kStages) {
     mbar_init(smem_u32(&full[tid / kStages][tid % kStages]), 1);
     mbar_init(smem_u32(&empty[tid / kStages][tid % kStages]), 1);
@@ -383,8 +383,8 @@ cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cu
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D><<<workers(D) / kPairs, kThreads, Geo<D>::kSmem, stream>>>(mk, mv, a, dm, box, l.hdr, l.part_o, l.part_ml);
-  return cudaGetLastError();
+  return launch_early(paged_decode_kernel<D>, workers(D) / kPairs, kThreads, Geo<D>::kSmem, stream, mk, mv, a, dm, box, l.hdr,
+                      l.part_o, l.part_ml);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@
 //
 // Measured: 300 tokens at 8300 keys, 32 / 8 heads of 128, 1.05 ms (38 TFLOP/s;
 // the FMA pipes are busy 57% of the time, shared memory 73%), three chunks of up to
-// 257 tokens with 16 heads of 64 122 us, where a fifth of the row tiles is padding.
+// 257 tokens with 16 heads of 64 120 us, where a fifth of the row tiles is padding.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_f32_kernel(PagedArgs a, Pag
   float* sv = sk + 2 * Gm::kKV;
   float* sp = sv + 2 * Gm::kKV;           // [64][BK + 4]
   const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
-  asm volatile("griddepcontrol.launch_dependents;\n" ::);
+  after_previous();
   const int64_t W = paged_plan<kBR, BK, kItemCost, kThreads>(plan, a.cu, a.kv_len, dm);
   const int64_t E = min((int64_t)kWorkers, (W + kMinTiles - 1) / kMinTiles), me = blockIdx.x;
   if (tid == 0) hdr[me].parts = 0;
@@ -251,8 +251,7 @@ template <int D>
 cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_f32_kernel<D><<<kWorkers, kThreads, Geo<D>::kSmem, stream>>>(a, dm, l.hdr, l.part_o, l.part_ml);
-  return cudaGetLastError();
+  return launch_early(paged_f32_kernel<D>, kWorkers, kThreads, Geo<D>::kSmem, stream, a, dm, l.hdr, l.part_o, l.part_ml);
 }
 
 }  // namespace
