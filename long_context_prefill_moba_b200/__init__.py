@@ -34,7 +34,7 @@ from typing import Optional
 import torch
 
 __all__ = [
-    "MobaShape", "MobaError", "lib", "load_library", "make_shape", "moba_check_shape",
+    "MobaShape", "MobaError", "lib", "load_library", "load_binding", "make_shape", "moba_check_shape",
     "moba_num_blocks", "moba_query_chunk", "moba_num_chunks", "moba_meank_elems",
     "moba_sel_elems", "moba_offsets_elems", "moba_rows_elems", "moba_gate_workspace_size",
     "moba_attn_workspace_size", "moba_block_meanpool", "moba_gate_topk", "moba_attn_fwd",

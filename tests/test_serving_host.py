@@ -145,7 +145,7 @@ def test_attention_pointers(L):
     assert M.moba_last_launch_count() == 0
 
 
-def test_binding_refuses_cpu_tensors():
+def test_binding_refuses_cpu_tensors(L):
     t = torch.zeros(3, 4, 64)
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
