@@ -510,8 +510,10 @@ template <typename T, int D>
 cudaError_t launch_fwd(RopeArgs a, bool append, cudaStream_t stream, int* launches) {
   constexpr int HPW = 512 / D;
   const int groups = (a.q == nullptr ? 0 : (a.hq + HPW - 1) / HPW) + (append ? 2 : 1) * ((a.hkv + HPW - 1) / HPW);
+  // a token's groups over several warps until two rounds of them fill the card: 6000 tokens of 32 / 8 heads take 28.0,
+  // 25.2, 26.8, 33.3 us with units up to 32, 64, 128, 192 an SM, 2000 tokens 10.5 to 11.1, 20000 all 70.5
   a.split = 1;
-  while (a.split * 2 <= groups && (int64_t)a.tokens * a.split < 32 * kSms && a.split < kWarps) a.split *= 2;
+  while (a.split * 2 <= groups && (int64_t)a.tokens * a.split < 64 * kSms && a.split < kWarps) a.split *= 2;
   const int64_t need = ((int64_t)a.tokens * a.split + kWarps - 1) / kWarps;
   const int64_t blocks = need < kFwdBlocks<T> * kSms ? need : kFwdBlocks<T> * kSms;
   if (blocks == 0) return cudaSuccess;
