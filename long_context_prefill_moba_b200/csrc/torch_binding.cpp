@@ -158,14 +158,22 @@ std::tuple<Tensor, Tensor> norm_rope(const Tensor& q, const Tensor& k, const Ten
 }
 
 // ---- paged cache ----------------------------------------------------------------
-moba_paged_shape_t paged_shape(const char* where, const Tensor& ref, int64_t hq, const Tensor& k_pool, const Tensor& v_pool,
-                               const Tensor& cu_new, const Tensor& kv_len, const Tensor& table, const optional<Tensor>& status,
-                               double scale) {
+// Pages one after another that do not overlap: a page's offset is its number times
+// the stride, and a stride of 0 (a page expanded over all) is the C call's "dense".
+void check_pools(const Tensor& k_pool, const Tensor& v_pool, const char* where) {
   REQUIRE(k_pool.dim() == 4 && k_pool.sizes() == v_pool.sizes(), where,
           "the pools must be [num_pages, heads, page_size, head_dim], alike");
   const int64_t pages = k_pool.size(0), hkv = k_pool.size(1), page = k_pool.size(2), d = k_pool.size(3);
-  for (const Tensor* p : {&k_pool, &v_pool})
+  for (const Tensor* p : {&k_pool, &v_pool}) {
     REQUIRE(p->stride(1) == page * d && p->stride(2) == d && p->stride(3) == 1, where, "a page of the pools must be dense");
+    REQUIRE(pages <= 1 || p->stride(0) >= hkv * page * d, where, "pages of the pools must not overlap");
+  }
+}
+
+moba_paged_shape_t paged_shape(const char* where, const Tensor& ref, int64_t hq, const Tensor& k_pool, const Tensor& v_pool,
+                               const Tensor& cu_new, const Tensor& kv_len, const Tensor& table, const optional<Tensor>& status,
+                               double scale) {
+  const int64_t pages = k_pool.size(0), hkv = k_pool.size(1), page = k_pool.size(2), d = k_pool.size(3);
   same(k_pool, ref, ref.scalar_type(), where, "k_pool");
   same(v_pool, ref, ref.scalar_type(), where, "v_pool");
   same(cu_new, ref, at::kInt, where, "cu_new");
@@ -193,9 +201,10 @@ optional<Tensor> cache_append(const Tensor& k_in, const Tensor& v_in, const Tens
                               const optional<Tensor>& q_in, const optional<Tensor>& q_weight, const optional<Tensor>& k_weight,
                               double eps, bool interleaved, const optional<Tensor>& status, optional<Tensor> q_out) {
   const char* where = "moba_cache_append";
+  check_pools(k_pool, v_pool, where);
   int64_t qs = 0, ks, vs;
   const Tensor k = rows(k_in, ks, where, "k"), v = rows(v_in, vs, where, "v");
-  REQUIRE(k.dim() == 3 && k.sizes() == v.sizes() && k_pool.dim() == 4 && k.size(1) == k_pool.size(1) && k.size(2) == k_pool.size(3),
+  REQUIRE(k.dim() == 3 && k.sizes() == v.sizes() && k.size(1) == k_pool.size(1) && k.size(2) == k_pool.size(3),
           where, "k and v must be [tokens, heads, head_dim] with the pools' heads");
   c10::DeviceGuard guard(k.device());
   same(v, k, k.scalar_type(), where, "v");
@@ -245,6 +254,7 @@ std::tuple<Tensor, optional<Tensor>> cache_attention(const Tensor& q_in, const T
                                                      optional<double> scale, bool return_lse, optional<Tensor> out,
                                                      const optional<Tensor>& status) {
   const char* where = "moba_cache_attention";
+  check_pools(k_pool, v_pool, where);
   int64_t qs;
   const Tensor q = rows(q_in, qs, where, "q");
   REQUIRE(q.dim() == 3, where, "q must be [tokens, heads, head_dim]");

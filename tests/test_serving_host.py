@@ -168,3 +168,21 @@ def test_binding_is_built_beside_the_library(L):
 def test_inv_freq():
     f = M.moba_rope_inv_freq(64, 10000.0, "cpu")
     assert f.dtype == torch.float64 and f.shape == (32,) and f[0] == 1.0 and abs(f[16] - 0.01) < 1e-15
+
+
+def test_pools_whose_pages_overlap_are_refused(L):
+    """A page for all (stride 0, which the C call reads as dense) and pages that overlap: no offset of a page may leave the
+    pool's memory."""
+    i = torch.zeros(2, dtype=torch.int32)
+    x, good = torch.zeros(3, 4, 64), torch.zeros(6, 4, 16, 64)
+    one = torch.zeros(1, 4, 16, 64).expand(6, 4, 16, 64)
+    half = torch.zeros(6 * 4 * 16 * 64).as_strided((6, 4, 16, 64), (2 * 16 * 64, 16 * 64, 64, 1))
+    for bad in (one, half):
+        for pools in ((bad, good), (good, bad)):
+            with pytest.raises(ValueError, match="overlap"):
+                M.moba_cache_append(x, x, i, i[:1], i[None], *pools)
+            with pytest.raises(ValueError, match="overlap"):
+                M.moba_cache_attention(x, *pools, i, i[:1], i[None])
+    # a single page has no stride that counts
+    with pytest.raises(ValueError, match="CUDA"):
+        M.moba_cache_attention(x, one[:1], good[:1], i, i[:1], i[None])
