@@ -45,15 +45,26 @@ int32_t i32(int64_t v, const char* where) {
 const void* ptr(const optional<Tensor>& t) { return t.has_value() ? t->const_data_ptr() : nullptr; }
 
 // x [..., h, d]: itself where its rows lie one stride apart on 16-byte borders
-// (part of a fused projection), else a dense copy; `step` elements between tokens
+// (part of a fused projection), else a dense copy; `step` elements between tokens.
+// Dimensions of size 1 are stepped over: their strides say nothing about the rows.
 Tensor rows(const Tensor& x, int64_t& step, const char* where, const char* name) {
   REQUIRE(x.dim() >= 3 && x.is_cuda(), where, name, " must be a CUDA tensor [..., heads, head_dim]");
   const auto size = x.sizes(), st = x.strides();
   const int64_t n = x.dim(), h = size[n - 2], d = size[n - 1];
-  step = st[n - 3];
-  bool ok = st[n - 1] == 1 && (h == 1 || st[n - 2] == d) && step >= h * d && step * x.element_size() % 16 == 0 &&
-            reinterpret_cast<uintptr_t>(x.const_data_ptr()) % 16 == 0;
-  for (int64_t i = 0; i + 3 < n && ok; ++i) ok = size[i] == 1 || st[i] == st[i + 1] * size[i + 1];
+  step = h * d;
+  bool ok = st[n - 1] == 1 && (h == 1 || st[n - 2] == d);
+  bool first = true;
+  int64_t next = 0;   // the stride that the dimension before must have
+  for (int64_t i = n - 3; i >= 0 && ok; --i) {
+    if (size[i] == 1) continue;
+    if (first)
+      step = st[i];
+    else
+      ok = st[i] == next;
+    first = false;
+    next = st[i] * size[i];
+  }
+  ok = ok && step >= h * d && step * x.element_size() % 16 == 0 && reinterpret_cast<uintptr_t>(x.const_data_ptr()) % 16 == 0;
   if (ok) return x;
   step = h * d;
   return x.clone(at::MemoryFormat::Contiguous);

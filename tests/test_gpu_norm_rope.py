@@ -264,3 +264,35 @@ def test_captured_step_and_another_stream(cuda_device):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, new))
     assert not torch.equal(got[0], want[0])
+
+
+def test_leading_dimensions_of_one(cuda_device):
+    """Dimensions of one token or sequence between others, whose strides say nothing about the rows: as dense inputs."""
+    import long_context_prefill_moba_b200 as M
+    dev = cuda_device
+    g = torch.Generator(device=dev)
+    g.manual_seed(6)
+    w, f = torch.ones(64, device=dev), M.moba_rope_inv_freq(64, device=dev)
+    views = [
+        lambda x: x[:, None, :5],          # [2, 1, 5, h, 64]: the stride of the 1 is that of the whole sequences
+        lambda x: x[:, :5, None],          # [2, 5, 1, h, 64]
+        lambda x: x[:, 3:4],               # one token of each sequence
+        lambda x: x[:1, 3:4],              # one token
+        lambda x: x[:1, None, 2:7],
+        lambda x: x[:, ::2][:, :, None],
+        lambda x: x[:, :, None, None],     # every token: read where it lies
+        lambda x: x[None, :, :5],
+        lambda x: x[:, 4:5].expand(2, 7, *x.shape[2:]),              # one token for all of a sequence
+        lambda x: x[:1, :6].expand(3, 6, *x.shape[2:])[:, None],     # one sequence for all
+        lambda x: x[:, 4:5, None].expand(2, 7, 3, *x.shape[2:]),
+    ]
+    for view in views:
+        q, k = (view(torch.randn(2, 10, h, 64, generator=g, device=dev)) for h in (4, 2))
+        pos = torch.arange(q.shape[:-2].numel(), dtype=torch.int32, device=dev)
+        dense = [x.contiguous().requires_grad_() for x in (q, k)]
+        leaves = [x.detach().requires_grad_() for x in (q, k)]
+        want, got = M.moba_norm_rope(*dense, w, w, pos, f), M.moba_norm_rope(*leaves, w, w, pos, f)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        d = [torch.randn(x.shape, generator=g, device=dev) for x in want]
+        a, b = torch.autograd.grad(got, leaves, d), torch.autograd.grad(want, dense, d)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
