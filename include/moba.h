@@ -388,7 +388,8 @@ typedef struct {
   moba_rope_t rope;
 } moba_rope_shape_t;
 
-/* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31). */
+/* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31, and a
+ * token's hq * head_dim < 2^31). */
 MOBA_API moba_status_t moba_check_rope_shape(const moba_rope_shape_t* shape);
 
 /* Norm and rotation of every query and key head, one kernel.
@@ -469,7 +470,7 @@ typedef struct {
 } moba_paged_shape_t;
 
 /* MOBA_OK if the shape is supported (host only; tokens * hq < 2^31,
- * max_pages * page_size <= 2^30). */
+ * hq * head_dim < 2^31, max_pages * page_size <= 2^30). */
 MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* shape);
 
 /* Appends the step's keys and values to the cache, keys (and queries, where

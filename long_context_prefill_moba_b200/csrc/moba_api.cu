@@ -647,7 +647,7 @@ MOBA_API moba_status_t moba_check_rope_shape(const moba_rope_shape_t* s) {
     return MOBA_ERR_INVALID_ARG;
   const moba_status_t st = check_rope(&s->rope, s->head_dim);
   if (st != MOBA_OK) return st;
-  if ((int64_t)s->tokens * s->hq > kI32Max) return MOBA_ERR_UNSUPPORTED;
+  if ((int64_t)s->tokens * s->hq > kI32Max || (int64_t)s->hq * s->head_dim > kI32Max) return MOBA_ERR_UNSUPPORTED;
   return MOBA_OK;
 }
 
@@ -721,7 +721,7 @@ MOBA_API moba_status_t moba_check_paged_shape(const moba_paged_shape_t* s) {
       !stride_ok(s->v_stride, kv, es) || !stride_ok(s->k_page_stride, page_dense(s), es) ||
       !stride_ok(s->v_page_stride, page_dense(s), es))
     return MOBA_ERR_INVALID_ARG;
-  if (s->batch > kGridYZMax || (int64_t)s->tokens * s->hq > kI32Max ||
+  if (s->batch > kGridYZMax || (int64_t)s->tokens * s->hq > kI32Max || (int64_t)s->hq * s->head_dim > kI32Max ||
       (int64_t)s->max_pages * s->page_size > kMaxPagedKeys)
     return MOBA_ERR_UNSUPPORTED;
   return MOBA_OK;

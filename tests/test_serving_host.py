@@ -186,3 +186,13 @@ def test_pools_whose_pages_overlap_are_refused(L):
     # a single page has no stride that counts
     with pytest.raises(ValueError, match="CUDA"):
         M.moba_cache_attention(x, one[:1], good[:1], i, i[:1], i[None])
+
+
+def test_a_row_of_heads_stays_in_32_bits(L):
+    for make, check in ((rope_shape, M.moba_check_rope_shape), (paged_shape, M.moba_check_paged_shape)):
+        for d, most in ((128, 2**24 - 1), (64, 2**25 - 1)):
+            kw = dict(tokens=1, hkv=1, head_dim=d)
+            if make is rope_shape:
+                kw["rot_dim"] = d
+            assert check(make(hq=most, **kw)) == OK
+            assert check(make(hq=most + 1, **kw)) == UNSUPPORTED
