@@ -436,7 +436,9 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(R
         u1 = f2_fma(xv[e + 1], f2_mul(z[e + 1], w[e + 1]), u1);
       }
       const float ss = head_sum<LPH>(f2_sum(f2_add(s0, s1))), dot = head_sum<LPH>(f2_sum(f2_add(u0, u1)));
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      // lanes without a head hold zeros, whose r would be infinite for eps = 0 and reach dw as 0 times an infinity
+      const int head = g * HPW + hl;
+      const float r = head < heads ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
       const float c = -(r * r * r * dot * (1.f / D));
       const uint64_t r2 = f2_pack(r, r), c2 = f2_pack(c, c);
 #pragma unroll
@@ -445,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(R
         dw[e] = f2_fma(rz, xv[e], dw[e]);
         z[e] = f2_fma(c2, xv[e], f2_mul(rz, w[e]));
       }
-      const int head = g * HPW + hl;
       if (head < heads) {
         T* p = dx + ((int64_t)t * heads + head) * D;
         d0.round(z); d1.round(z + 4);

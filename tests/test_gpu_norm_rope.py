@@ -296,3 +296,20 @@ def test_leading_dimensions_of_one(cuda_device):
         d = [torch.randn(x.shape, generator=g, device=dev) for x in want]
         a, b = torch.autograd.grad(got, leaves, d), torch.autograd.grad(want, dense, d)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("case", [
+    (9, 5, 1, 128, 128, False, "bf16", "bf16", 50), (40, 6, 3, 64, 64, True, "f32", "f32", 50),
+    (300, 2, 2, 128, 64, False, "f32", "f32", 300), (17, 9, 9, 64, 0, False, "bf16", "f32", 50)], ids=str)
+def test_gradients_without_eps(cuda_device, case):
+    """eps = 0, head counts that leave lanes of a warp without a head."""
+    import long_context_prefill_moba_b200 as M
+    T, hq, hkv, d, rot, inter, dt, wt, far = case
+    q, k, wq, wk, pos, f, dq, dk = inputs(case, cuda_device, 7)
+    leaves = [x.detach().requires_grad_() for x in (q, k, wq, wk)]
+    outs = M.moba_norm_rope(*leaves, pos, f, 0.0, inter)
+    check_forward(outs[0], q, wq, pos, f, 0.0, inter, q.dtype)
+    check_forward(outs[1], k, wk, pos, f, 0.0, inter, q.dtype)
+    grads = torch.autograd.grad(outs, leaves, (dq, dk))
+    check_backward(grads[0], grads[2], q, wq, pos, f, 0.0, dq, inter, q.dtype, wq.dtype)
+    check_backward(grads[1], grads[3], k, wk, pos, f, 0.0, dk, inter, q.dtype, wq.dtype)
