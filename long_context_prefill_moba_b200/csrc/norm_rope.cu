@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) norm_rope_bwd_kernel(R
       // lanes without a head hold zeros, whose r would be infinite for eps = 0 and reach dw as 0 times an infinity
       const int head = g * HPW + hl;
       const float r = head < heads ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-      const float c = -(r * r * r * dot * (1.f / D));
+      const float c = -(r * dot * (1.f / D)) * r * r;   // r^3 alone leaves fp32 outside 3e-13 .. 6e12
       const uint64_t r2 = f2_pack(r, r), c2 = f2_pack(c, c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

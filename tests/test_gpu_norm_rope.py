@@ -313,3 +313,18 @@ def test_gradients_without_eps(cuda_device, case):
     grads = torch.autograd.grad(outs, leaves, (dq, dk))
     check_backward(grads[0], grads[2], q, wq, pos, f, 0.0, dq, inter, q.dtype, wq.dtype)
     check_backward(grads[1], grads[3], k, wk, pos, f, 0.0, dk, inter, q.dtype, wq.dtype)
+
+
+@pytest.mark.parametrize("size,eps", [(1e-17, 0.0), (1e-12, 0.0), (1e13, 1e-6), (1e15, 1e-6), (1e17, 1e-6), (0.0, 1e-30)])
+def test_gradients_of_small_and_large_heads(cuda_device, size, eps):
+    """Heads whose squares fit fp32 but whose r^3 does not: no product of the gradient leaves the normal range, so the
+    bounds are those of heads of size 1."""
+    import long_context_prefill_moba_b200 as M
+    case = (11, 4, 2, 64, 64, False, "f32", "f32", 50)
+    q, k, wq, wk, pos, f, dq, dk = inputs(case, cuda_device, 8)
+    q, k = (size * x for x in (q, k))
+    leaves = [x.detach().requires_grad_() for x in (q, k, wq, wk)]
+    outs = M.moba_norm_rope(*leaves, pos, f, eps)
+    grads = torch.autograd.grad(outs, leaves, (dq, dk))
+    check_backward(grads[0], grads[2], q, wq, pos, f, eps, dq, False, q.dtype, wq.dtype)
+    check_backward(grads[1], grads[3], k, wk, pos, f, eps, dk, False, q.dtype, wq.dtype)
