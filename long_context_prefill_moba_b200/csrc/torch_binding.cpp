@@ -42,6 +42,12 @@ int32_t i32(int64_t v, const char* where) {
   REQUIRE(v >= 0 && v <= INT32_MAX, where, "a size beyond 32 bits");
   return (int32_t)v;
 }
+// a tangent (forward-mode AD) does not make a tensor require a gradient, and would be lost
+void no_tangents(std::initializer_list<const Tensor*> ts, const char* where) {
+  for (const Tensor* t : ts)
+    TORCH_CHECK(t == nullptr || !t->_fw_grad(/*level=*/0).defined(), where, ": has no forward-mode derivative");
+}
+const Tensor* ptr_or_null(const optional<Tensor>& t) { return t.has_value() ? &*t : nullptr; }
 const void* ptr(const optional<Tensor>& t) { return t.has_value() ? t->const_data_ptr() : nullptr; }
 
 // x [..., h, d]: itself where its rows lie one stride apart on 16-byte borders
@@ -134,6 +140,7 @@ struct NormRope : torch::autograd::Function<NormRope> {
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
     const char* where = "moba_norm_rope";
     TORCH_CHECK(!at::GradMode::is_enabled(), where, ": its gradients are not differentiable (create_graph)");
+    no_tangents({&grads[0], &grads[1]}, where);
     const auto saved = ctx->get_saved_variables();
     const Tensor &qw = saved[2], &kw = saved[3], &positions = saved[4], &inv_freq = saved[5];
     const NormRopeArgs a = norm_rope_args(saved[0], saved[1], qw, kw, positions, inv_freq, ctx->saved_data["eps"].toDouble(),
@@ -159,6 +166,7 @@ struct NormRope : torch::autograd::Function<NormRope> {
 
 std::tuple<Tensor, Tensor> norm_rope(const Tensor& q, const Tensor& k, const Tensor& q_weight, const Tensor& k_weight,
                                      const Tensor& positions, const Tensor& inv_freq, double eps, bool interleaved) {
+  no_tangents({&q, &k, &q_weight, &k_weight, &inv_freq}, "moba_norm_rope");
   if (at::GradMode::is_enabled() &&
       (q.requires_grad() || k.requires_grad() || q_weight.requires_grad() || k_weight.requires_grad())) {
     const auto out = NormRope::apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved);
@@ -212,6 +220,9 @@ optional<Tensor> cache_append(const Tensor& k_in, const Tensor& v_in, const Tens
                               const optional<Tensor>& q_in, const optional<Tensor>& q_weight, const optional<Tensor>& k_weight,
                               double eps, bool interleaved, const optional<Tensor>& status, optional<Tensor> q_out) {
   const char* where = "moba_cache_append";
+  no_tangents({&k_in, &v_in, ptr_or_null(q_in), ptr_or_null(q_weight), ptr_or_null(k_weight), &k_pool, &v_pool,
+               ptr_or_null(inv_freq), ptr_or_null(q_out)},
+              where);
   check_pools(k_pool, v_pool, where);
   int64_t qs = 0, ks, vs;
   const Tensor k = rows(k_in, ks, where, "k"), v = rows(v_in, vs, where, "v");
@@ -265,6 +276,7 @@ std::tuple<Tensor, optional<Tensor>> cache_attention(const Tensor& q_in, const T
                                                      optional<double> scale, bool return_lse, optional<Tensor> out,
                                                      const optional<Tensor>& status) {
   const char* where = "moba_cache_attention";
+  no_tangents({&q_in, &k_pool, &v_pool, ptr_or_null(out)}, where);
   check_pools(k_pool, v_pool, where);
   int64_t qs;
   const Tensor q = rows(q_in, qs, where, "q");

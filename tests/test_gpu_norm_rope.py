@@ -328,3 +328,26 @@ def test_gradients_of_small_and_large_heads(cuda_device, size, eps):
     grads = torch.autograd.grad(outs, leaves, (dq, dk))
     check_backward(grads[0], grads[2], q, wq, pos, f, eps, dq, False, q.dtype, wq.dtype)
     check_backward(grads[1], grads[3], k, wk, pos, f, eps, dk, False, q.dtype, wq.dtype)
+
+
+def test_forward_mode_derivatives_are_refused(cuda_device):
+    """Tangents of the inputs, and of the gradients that a backward pass is given."""
+    import torch.autograd.forward_ad as fwad
+    import long_context_prefill_moba_b200 as M
+    q, k, wq, wk, pos, f, dq, dk = inputs((3, 4, 2, 64, 64, False, "f32", "f32", 50), cuda_device)
+    args = [x.contiguous() for x in (q, k, wq, wk)]
+    for at in range(4):
+        for grad in (False, True):
+            with fwad.dual_level():
+                dual = [x.detach().clone().requires_grad_(grad) for x in args]
+                dual[at] = fwad.make_dual(dual[at], torch.ones_like(args[at]))
+                with pytest.raises(RuntimeError, match="forward-mode"):
+                    M.moba_norm_rope(*dual, pos, f)
+    leaves = [x.detach().clone().requires_grad_() for x in args]
+    outs = M.moba_norm_rope(*leaves, pos, f)
+    want = torch.autograd.grad(outs, leaves, (dq, dk), retain_graph=True)
+    with fwad.dual_level():
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            torch.autograd.grad(outs, leaves, (fwad.make_dual(dq, torch.ones_like(dq)), dk), retain_graph=True)
+    again = torch.autograd.grad(outs, leaves, (dq, dk))
+    assert all(torch.equal(a, b) for a, b in zip(want, again))

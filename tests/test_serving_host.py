@@ -196,3 +196,22 @@ def test_a_row_of_heads_stays_in_32_bits(L):
                 kw["rot_dim"] = d
             assert check(make(hq=most, **kw)) == OK
             assert check(make(hq=most + 1, **kw)) == UNSUPPORTED
+
+
+def test_forward_mode_derivatives_are_refused(L):
+    """A dual tensor needs no gradient in reverse mode; its tangent must not be lost either."""
+    import torch.autograd.forward_ad as fwad
+    t, w, i = torch.zeros(3, 4, 64), torch.ones(64), torch.zeros(2, dtype=torch.int32)
+    f, pool = torch.zeros(0, dtype=torch.float64), torch.zeros(2, 4, 16, 64)
+    norm = lambda q, k, wq, wk: M.moba_norm_rope(q, k, wq, wk, i, f)  # noqa: E731
+    append = lambda k, v, q, wq, wk, kp: M.moba_cache_append(k, v, i, i[:1], i[None], kp, pool, q=q, q_weight=wq, k_weight=wk)  # noqa: E731
+    attend = lambda q, kp, vp: M.moba_cache_attention(q, kp, vp, i, i[:1], i[None])  # noqa: E731
+    for call, args in ((norm, (t, t, w, w)), (append, (t, t, t, w, w, pool)), (attend, (t, pool, pool))):
+        for at in range(len(args)):
+            with fwad.dual_level():
+                dual = list(args)
+                dual[at] = fwad.make_dual(args[at], torch.ones_like(args[at]))
+                with pytest.raises(RuntimeError, match="forward-mode"):
+                    call(*dual)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(*args)
