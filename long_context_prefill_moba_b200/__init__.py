@@ -694,7 +694,9 @@ def moba_cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq=None
     int32 [batch] (new tokens included), table int32 [batch, max_pages].  `status`: a
     zeroed int32 CUDA tensor that becomes nonzero if a token had no page.  Returns the
     queries (None without q): q_out, or a new tensor whose rows from cu_new[-1] on
-    are not written.  Runs on the current stream of k's device."""
+    are not written.  For serving: there is no gradient, and inputs that require one
+    (a module's parameters) are refused outside torch.no_grad().  Runs on the current
+    stream of k's device."""
     return (_binding or load_binding()).cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq, q, q_weight,
                                                      k_weight, eps, interleaved, status, q_out)
 
@@ -706,7 +708,8 @@ def moba_cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale=None, r
 
     q [T, Hq, d]; the other arguments as for moba_cache_append.  Returns out [T, Hq, d],
     with return_lse also the log-sum-exp [Hq, T] in fp32; rows from cu_new[-1] on are
-    not written.  The workspace comes from torch's allocator, so that calls on
+    not written.  There is no gradient, and inputs that require one are refused outside
+    torch.no_grad().  The workspace comes from torch's allocator, so that calls on
     several streams, and captured graphs, have one each.  Runs on the current stream
     of q's device."""
     out, lse = (_binding or load_binding()).cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale, return_lse, out,

@@ -47,6 +47,13 @@ void no_tangents(std::initializer_list<const Tensor*> ts, const char* where) {
   for (const Tensor* t : ts)
     TORCH_CHECK(t == nullptr || !t->_fw_grad(/*level=*/0).defined(), where, ": has no forward-mode derivative");
 }
+// the cache's calls have no backward pass: an input that asks for a gradient would be cut off
+void no_gradients(std::initializer_list<const Tensor*> ts, const char* where) {
+  no_tangents(ts, where);
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : ts)
+    TORCH_CHECK(t == nullptr || !t->requires_grad(), where, ": has no gradient; call it under torch.no_grad() or detach its inputs");
+}
 const Tensor* ptr_or_null(const optional<Tensor>& t) { return t.has_value() ? &*t : nullptr; }
 const void* ptr(const optional<Tensor>& t) { return t.has_value() ? t->const_data_ptr() : nullptr; }
 
@@ -220,9 +227,9 @@ optional<Tensor> cache_append(const Tensor& k_in, const Tensor& v_in, const Tens
                               const optional<Tensor>& q_in, const optional<Tensor>& q_weight, const optional<Tensor>& k_weight,
                               double eps, bool interleaved, const optional<Tensor>& status, optional<Tensor> q_out) {
   const char* where = "moba_cache_append";
-  no_tangents({&k_in, &v_in, ptr_or_null(q_in), ptr_or_null(q_weight), ptr_or_null(k_weight), &k_pool, &v_pool,
-               ptr_or_null(inv_freq), ptr_or_null(q_out)},
-              where);
+  no_gradients({&k_in, &v_in, ptr_or_null(q_in), ptr_or_null(q_weight), ptr_or_null(k_weight), &k_pool, &v_pool,
+                ptr_or_null(inv_freq), ptr_or_null(q_out)},
+               where);
   check_pools(k_pool, v_pool, where);
   int64_t qs = 0, ks, vs;
   const Tensor k = rows(k_in, ks, where, "k"), v = rows(v_in, vs, where, "v");
@@ -276,7 +283,7 @@ std::tuple<Tensor, optional<Tensor>> cache_attention(const Tensor& q_in, const T
                                                      optional<double> scale, bool return_lse, optional<Tensor> out,
                                                      const optional<Tensor>& status) {
   const char* where = "moba_cache_attention";
-  no_tangents({&q_in, &k_pool, &v_pool, ptr_or_null(out)}, where);
+  no_gradients({&q_in, &k_pool, &v_pool, ptr_or_null(out)}, where);
   check_pools(k_pool, v_pool, where);
   int64_t qs;
   const Tensor q = rows(q_in, qs, where, "q");

@@ -505,3 +505,29 @@ def test_refusals_with_device_tensors(cuda_device):
                 dict(k_weight=torch.ones(32, device=dev)), dict(inv_freq=M.moba_rope_inv_freq(128, device=dev))):
         with pytest.raises((ValueError, M.MobaError)):
             M.moba_cache_append(**{**good, **bad})
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_weights_of_a_module_without_gradients(cuda_device, new):
+    """Parameters serve under no_grad or inference_mode, or detached; in grad mode the calls refuse them."""
+    import long_context_prefill_moba_b200 as M
+    c = Cache([(new, 90)], 16, 2, 64, "bf16", cuda_device, nan=False)
+    x = c.rand(new, 8, 64)
+    w = torch.nn.Parameter(1 + 0.3 * torch.randn(64, generator=c.g).to(cuda_device))
+
+    def step(x, w):
+        q = M.moba_cache_append(x[:, 4:6], x[:, 6:], *c.index, c.k_pool, c.v_pool, q=x[:, :4], q_weight=w, k_weight=w)
+        return M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index)
+
+    want = step(x, w.detach())
+    with torch.no_grad():
+        assert torch.equal(step(x, w), want)
+    with torch.inference_mode():
+        assert torch.equal(step(x, w), want)
+    before = c.k_pool.clone()
+    with pytest.raises(RuntimeError, match="no gradient"):
+        step(x, w)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        M.moba_cache_attention(x[:, :4].clone().requires_grad_(), c.k_pool, c.v_pool, *c.index)
+    torch.cuda.synchronize()
+    assert torch.equal(c.k_pool, before)

@@ -215,3 +215,19 @@ def test_forward_mode_derivatives_are_refused(L):
                     call(*dual)
         with pytest.raises(ValueError, match="CUDA"):
             call(*args)
+
+
+def test_cache_calls_refuse_gradients(L):
+    """They have none: an input that asks for one is refused in grad mode, not cut off without a word."""
+    t, w, i = torch.zeros(3, 4, 64), torch.ones(64), torch.zeros(2, dtype=torch.int32)
+    pool = torch.zeros(2, 4, 16, 64)
+    append = lambda k, v, q, wq, wk, kp, vp: M.moba_cache_append(k, v, i, i[:1], i[None], kp, vp, q=q, q_weight=wq, k_weight=wk)  # noqa: E731
+    attend = lambda q, kp, vp: M.moba_cache_attention(q, kp, vp, i, i[:1], i[None])  # noqa: E731
+    for call, args in ((append, (t, t, t, w, w, pool, pool)), (attend, (t, pool, pool))):
+        for at in range(len(args)):
+            asks = list(args)
+            asks[at] = args[at].clone().requires_grad_()
+            with pytest.raises(RuntimeError, match="no gradient"):
+                call(*asks)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(*asks)
