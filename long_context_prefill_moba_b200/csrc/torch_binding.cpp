@@ -55,6 +55,12 @@ void no_gradients(std::initializer_list<const Tensor*> ts, const char* where) {
     TORCH_CHECK(t == nullptr || !t->requires_grad(), where, ": has no gradient; call it under torch.no_grad() or detach its inputs");
 }
 const Tensor* ptr_or_null(const optional<Tensor>& t) { return t.has_value() ? &*t : nullptr; }
+// tensors of the caller that a call wrote: autograd finds out by their versions
+// (which inference tensors do not keep) that a value it saved is gone
+void written(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 const void* ptr(const optional<Tensor>& t) { return t.has_value() ? t->const_data_ptr() : nullptr; }
 
 // x [..., h, d]: itself where its rows lie one stride apart on 16-byte borders
@@ -275,6 +281,7 @@ optional<Tensor> cache_append(const Tensor& k_in, const Tensor& v_in, const Tens
                           k_pool.mutable_data_ptr(), v_pool.mutable_data_ptr(),
                           status.has_value() ? (int*)status->mutable_data_ptr() : nullptr, stream()),
         where);
+  written({&k_pool, &v_pool, ptr_or_null(q_out), ptr_or_null(status)});
   return q_out;
 }
 
@@ -308,6 +315,7 @@ std::tuple<Tensor, optional<Tensor>> cache_attention(const Tensor& q_in, const T
                         lse.has_value() ? lse->mutable_data_ptr<float>() : nullptr,
                         status.has_value() ? (int*)status->mutable_data_ptr() : nullptr, ws.mutable_data_ptr(), bytes, stream()),
         where);
+  written({&*out, ptr_or_null(status)});
   return {*out, lse};
 }
 

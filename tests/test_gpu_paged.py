@@ -531,3 +531,46 @@ def test_weights_of_a_module_without_gradients(cuda_device, new):
         M.moba_cache_attention(x[:, :4].clone().requires_grad_(), c.k_pool, c.v_pool, *c.index)
     torch.cuda.synchronize()
     assert torch.equal(c.k_pool, before)
+
+
+def test_written_tensors_raise_their_version(cuda_device):
+    """A tensor that a backward pass has saved and a call then overwrites is found out by autograd."""
+    import long_context_prefill_moba_b200 as M
+    for new in (1, 40):
+        c = Cache([(new, 90)], 16, 2, 64, "bf16", cuda_device, nan=False)
+        x = c.rand(new, 4, 64)
+        q = c.rand(new, 4, 64)
+        status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+        k_pool, v_pool, out = c.k_pool.clone(), c.v_pool.clone(), torch.empty_like(q)
+        at = [t._version for t in (k_pool, v_pool, q, out, status)]
+        M.moba_cache_append(x[:, :2], x[:, 2:], *c.index, k_pool, v_pool, q=q, q_out=q, status=status)
+        M.moba_cache_attention(q, k_pool, v_pool, *c.index, out=out, status=status)
+        assert all(t._version > v for t, v in zip((k_pool, v_pool, q, out, status), at))
+        w = torch.ones_like(q, requires_grad=True)
+        loss = (w * out).sum()          # saves `out`
+        M.moba_cache_attention(q, k_pool, v_pool, *c.index, out=out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        # inputs are only read
+        at = q._version
+        M.moba_cache_attention(q, k_pool, v_pool, *c.index)
+        assert q._version == at
+
+
+def test_buffers_made_in_inference_mode(cuda_device):
+    """They keep no versions, and serve in and out of the mode."""
+    import long_context_prefill_moba_b200 as M
+    c = Cache([(2, 90)], 16, 2, 64, "bf16", cuda_device, nan=False)
+    x = c.rand(2, 8, 64)
+    with torch.inference_mode():
+        k_pool, v_pool, q_out, out = c.k_pool.clone(), c.v_pool.clone(), torch.empty(2, 4, 64, dtype=c.dtype, device=cuda_device), None
+
+    def step(k_pool, v_pool, q_out):
+        q = M.moba_cache_append(x[:, 4:6], x[:, 6:], *c.index, k_pool, v_pool, q=x[:, :4], q_out=q_out)
+        return M.moba_cache_attention(q, k_pool, v_pool, *c.index)
+
+    want = step(c.k_pool, c.v_pool, None)
+    assert torch.equal(step(k_pool, v_pool, q_out), want)
+    with torch.inference_mode():
+        assert torch.equal(step(k_pool, v_pool, q_out), want)
+    assert torch.equal(k_pool, c.k_pool) and torch.equal(v_pool, c.v_pool)
