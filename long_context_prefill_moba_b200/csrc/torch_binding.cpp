@@ -197,7 +197,8 @@ void check_pools(const Tensor& k_pool, const Tensor& v_pool, const char* where) 
           "the pools must be [num_pages, heads, page_size, head_dim], alike");
   const int64_t pages = k_pool.size(0), hkv = k_pool.size(1), page = k_pool.size(2), d = k_pool.size(3);
   for (const Tensor* p : {&k_pool, &v_pool}) {
-    REQUIRE(p->stride(1) == page * d && p->stride(2) == d && p->stride(3) == 1, where, "a page of the pools must be dense");
+    REQUIRE((hkv == 1 || p->stride(1) == page * d) && p->stride(2) == d && p->stride(3) == 1, where,
+            "a page of the pools must be dense");
     REQUIRE(pages <= 1 || p->stride(0) >= hkv * page * d, where, "pages of the pools must not overlap");
   }
 }

@@ -574,3 +574,20 @@ def test_buffers_made_in_inference_mode(cuda_device):
     with torch.inference_mode():
         assert torch.equal(step(k_pool, v_pool, q_out), want)
     assert torch.equal(k_pool, c.k_pool) and torch.equal(v_pool, c.v_pool)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 50])
+def test_one_kv_head_in_slots_before_heads(cuda_device, dt, new):
+    """Pools of one head kept as [pages, slots, 1, d]: as the dense ones."""
+    import long_context_prefill_moba_b200 as M
+    c = Cache([(new, 200), (new, 77)], 16, 1, 64, dt, cuda_device, nan=False)
+    x = c.rand(c.rows, 6, 64)
+    pools = [torch.empty(c.pages, 16, 1, 64, dtype=c.dtype, device=cuda_device).transpose(1, 2).copy_(p)
+             for p in (c.k_pool, c.v_pool)]
+    assert pools[0].stride(1) != 16 * 64
+    got = []
+    for k_pool, v_pool in ((c.k_pool, c.v_pool), pools):
+        q = M.moba_cache_append(x[:, 4:5], x[:, 5:], *c.index, k_pool, v_pool, q=x[:, :4])
+        got.append(M.moba_cache_attention(q, k_pool, v_pool, *c.index))
+    assert torch.equal(*got) and torch.equal(pools[0], c.k_pool) and torch.equal(pools[1], c.v_pool)

@@ -231,3 +231,16 @@ def test_cache_calls_refuse_gradients(L):
                 call(*asks)
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
                 call(*asks)
+
+
+def test_a_single_heads_stride_does_not_count(L):
+    """Pools kept as [pages, slots, 1, d] and passed with heads and slots exchanged are dense."""
+    i = torch.zeros(2, dtype=torch.int32)
+    x, pool = torch.zeros(3, 1, 64), torch.zeros(6, 16, 1, 64).transpose(1, 2)
+    assert pool.stride(1) != 16 * 64
+    with pytest.raises(ValueError, match="CUDA"):
+        M.moba_cache_append(x, x, i, i[:1], i[None], pool, pool)
+    with pytest.raises(ValueError, match="CUDA"):
+        M.moba_cache_attention(x, pool, pool, i, i[:1], i[None])
+    with pytest.raises(ValueError, match="dense"):
+        M.moba_cache_attention(torch.zeros(3, 4, 64), *[torch.zeros(6, 16, 4, 64).transpose(1, 2)] * 2, i, i[:1], i[None])
