@@ -41,12 +41,12 @@
 // it issued, frees TMEM and reports MOBA_ERR_TIMEOUT through the status word.
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 
 namespace moba {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // attn_tc.cu
 
 namespace {
 
@@ -768,7 +768,7 @@ cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cu
       !make_pool_map(&mv, a.v_pool, dm, D, dm.v_page_stride, box))
     return cudaErrorInvalidValue;
   // the setmaxnreg split is only safe if the kernel launches with kLaunchRegs
-  static int regs = -1;
+  static std::atomic<int> regs{-1};   // calls may come from several threads
   if (regs < 0) {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, paged_tc_kernel<D>);
@@ -780,6 +780,18 @@ cudaError_t launch(const PagedDims& dm, const PagedArgs& a, const PagedWs& l, cu
   if (e != cudaSuccess) return e;
   return launch_early(paged_tc_kernel<D>, kWorkers, kThreads, Geo<D>::kSmem, stream, mk, mv, a, dm, box, l.hdr, l.part_o,
                       l.part_ml);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
 }
 
 }  // namespace

@@ -22,14 +22,10 @@
 // In tiles that some row does not see whole, slots behind the sequence's end and
 // non-finite values are cleared first and the latter added at the end to the
 // rows that see them (0 times an infinity is not 0).
-#include <cudaTypedefs.h>
-
 #include "paged.cuh"
 #include "sm100.cuh"
 
 namespace moba {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // attn_tc.cu
 
 namespace {
 

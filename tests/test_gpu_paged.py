@@ -591,3 +591,28 @@ def test_one_kv_head_in_slots_before_heads(cuda_device, dt, new):
         q = M.moba_cache_append(x[:, 4:5], x[:, 5:], *c.index, k_pool, v_pool, q=x[:, :4])
         got.append(M.moba_cache_attention(q, k_pool, v_pool, *c.index))
     assert torch.equal(*got) and torch.equal(pools[0], c.k_pool) and torch.equal(pools[1], c.v_pool)
+
+
+def test_calls_from_two_threads(cuda_device):
+    """Threads of one process, each with its own stream: the calls give the interpreter's lock back while they run."""
+    import threading
+    import long_context_prefill_moba_b200 as M
+    cs = [Cache([(n, 300), (n, 150)], 32, 2, d, "bf16", cuda_device, seed=d + n) for d in (64, 128) for n in (1, 90)]
+    qs = [c.rand(c.rows, 8, c.d) for c in cs]
+    got = {}
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got[i] = [M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index) for _ in range(20) for c, q in zip(cs, qs)]
+        stream.synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    want = [M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index) for c, q in zip(cs, qs)]
+    for i in range(2):
+        assert len(got[i]) == 80 and all(torch.equal(x, want[j % 4]) for j, x in enumerate(got[i]))
