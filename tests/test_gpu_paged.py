@@ -616,3 +616,16 @@ def test_calls_from_two_threads(cuda_device):
     want = [M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index) for c, q in zip(cs, qs)]
     for i in range(2):
         assert len(got[i]) == 80 and all(torch.equal(x, want[j % 4]) for j, x in enumerate(got[i]))
+
+
+@pytest.mark.parametrize("dt,d,chunk", [("bf16", 128, 400), ("bf16", 64, 333), ("f32", 128, 300), ("f32", 64, 401)])
+def test_a_chunk_among_single_tokens(cuda_device, dt, d, chunk):
+    """Few rows a sequence on average, so that the kernels for single tokens take the chunk's long run of row tiles too."""
+    import long_context_prefill_moba_b200 as M
+    lens = [(1, 200 + 17 * i) for i in range(40)] + [(chunk, chunk + 900)] + [(1, 33)] * 30 + [(0, 5)] * 4
+    hq, hkv = 8, 2
+    assert sum(n for n, _ in lens) * (hq // hkv) <= 32 * len(lens)
+    c = Cache(lens, 32, hkv, d, dt, cuda_device, pad=2)
+    q = c.rand(c.rows, hq, d)
+    out, lse = M.moba_cache_attention(q, c.k_pool, c.v_pool, *c.index, return_lse=True)
+    check_attention(c, q, out, lse, rows=list(range(0, 40, 7)) + list(range(39, c.total, 23)) + [39 + chunk, c.total - 1])
