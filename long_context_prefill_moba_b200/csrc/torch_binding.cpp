@@ -180,6 +180,7 @@ struct NormRope : torch::autograd::Function<NormRope> {
 std::tuple<Tensor, Tensor> norm_rope(const Tensor& q, const Tensor& k, const Tensor& q_weight, const Tensor& k_weight,
                                      const Tensor& positions, const Tensor& inv_freq, double eps, bool interleaved) {
   no_tangents({&q, &k, &q_weight, &k_weight, &inv_freq}, "moba_norm_rope");
+  TORCH_CHECK(!at::GradMode::is_enabled() || !inv_freq.requires_grad(), "moba_norm_rope: inv_freq has no gradient; detach it");
   if (at::GradMode::is_enabled() &&
       (q.requires_grad() || k.requires_grad() || q_weight.requires_grad() || k_weight.requires_grad())) {
     const auto out = NormRope::apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved);

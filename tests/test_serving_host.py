@@ -244,3 +244,12 @@ def test_a_single_heads_stride_does_not_count(L):
         M.moba_cache_attention(x, pool, pool, i, i[:1], i[None])
     with pytest.raises(ValueError, match="dense"):
         M.moba_cache_attention(torch.zeros(3, 4, 64), *[torch.zeros(6, 16, 4, 64).transpose(1, 2)] * 2, i, i[:1], i[None])
+
+
+def test_frequencies_have_no_gradient(L):
+    t, w, i = torch.zeros(2, 4, 64), torch.ones(64), torch.zeros(2, dtype=torch.int32)
+    f = torch.ones(32, dtype=torch.float64, requires_grad=True)
+    with pytest.raises(RuntimeError, match="inv_freq has no gradient"):
+        M.moba_norm_rope(t, t, w, w, i, f)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        M.moba_norm_rope(t, t, w, w, i, f)
