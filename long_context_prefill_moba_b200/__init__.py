@@ -673,7 +673,7 @@ def load_binding():
 
 def moba_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False):
     """Norm of every query and key head and the position rotation, in one pass and
-    differentiable (once) in q, k and the weights: what precedes moba_attention in a layer.
+    differentiable (once, in reverse mode) in q, k and the weights: what precedes moba_attention in a layer.
 
     q [..., Hq, d], k [..., Hkv, d] with the same leading dimensions (rows of a fused
     projection are read where they lie), q_weight/k_weight [d], positions int32 with
@@ -704,11 +704,15 @@ def moba_cache_append(k, v, cu_new, kv_len, table, k_pool, v_pool, inv_freq=None
 def moba_cache_attention(q, k_pool, v_pool, cu_new, kv_len, table, scale=None, return_lse=False, out=None, status=None):
     """Causal attention of a step's new tokens over the paged cache that holds them
     (moba_cache_append): one token a sequence is a decode step, any mix of lengths
-    one call.
+    one call (the kernel goes by the average number of rows a sequence, padding and
+    sequences without new tokens included: long chunks and many single tokens are up to
+    twice as fast in a call each).
 
-    q [T, Hq, d]; the other arguments as for moba_cache_append.  Returns out [T, Hq, d],
-    with return_lse also the log-sum-exp [Hq, T] in fp32; rows from cu_new[-1] on are
-    not written.  There is no gradient, and inputs that require one are refused outside
+    q [T, Hq, d]; the other arguments as for moba_cache_append.  scale: None, or 0 and
+    below, is 1/sqrt(d).  Returns out [T, Hq, d] (not q's memory), with return_lse also
+    the log-sum-exp [Hq, T] in fp32; rows from cu_new[-1] on are not written.  Keys of a
+    page that the pool does not have count as zeros, and a length beyond the table is cut
+    to it: only `status` tells.  There is no gradient, and inputs that require one are refused outside
     torch.no_grad().  The workspace comes from torch's allocator, so that calls on
     several streams, and captured graphs, have one each.  Runs on the current stream
     of q's device."""

@@ -19,10 +19,11 @@
 // Sums are fp32; results are rounded once, on the store.
 //
 // Measured (bf16, 32768 tokens, 32 / 8 heads of 128; the copy benchmark moves 6.56
-// TB/s): forward 0.67 GB in 112 us (6.0 TB/s), backward 1.01 GB in 178 us (5.65),
-// weight gradients' rows 6 us more.  The forward waits for loads and issues at 70%
-// of its slots; the backward's 128 registers hold it to 16 warps an SM, and less
-// registers spill.  Append of 16K tokens with the norm: 0.40 GB in 75 us (5.3 TB/s).
+// TB/s): forward 0.67 GB in 112 to 114 us (5.9 TB/s), backward 1.01 GB in 178 us (5.65),
+// weight gradients' rows 6 us more.  fp32, 12000 tokens of the same heads: forward
+// 90 us (5.5 TB/s), backward with the rows 129 (5.7).  The forward waits for loads
+// and issues at 70% of its slots; the backward's 128 registers hold it to 16 warps an
+// SM, and less registers spill.  Append of 16K tokens with the norm: 0.40 GB in 75 us (5.3 TB/s).
 #include "launch.h"
 #include "sm100.cuh"
 

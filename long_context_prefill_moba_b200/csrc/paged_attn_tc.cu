@@ -27,13 +27,13 @@
 //
 // Bound: the exponentials (16 a clock and SM) and the MMAs of a tile take 2048
 // clocks each at D = 128 and overlap only in part, since S(i+1) cannot be issued
-// before P(i), which lies in its place, is read.  Measured (32 / 8 heads of 128):
-// 4096 tokens at 131072 in 7.7 ms, 1120 TFLOP/s (0.81 of the library product's
-// sustained rate, both under the power cap), 2048 at 65536 in 1.84 ms (1177); a
-// prompt of 8192 tokens 544 us (1010), of 2048 75 us (457), where setting up (6 us),
-// queries, mask and epilogue of each item (some 5 us) and the joining of cut items
-// (8 us) count.  At D = 64 the MMAs take half, the exponentials the same: 490
-// TFLOP/s.
+// before P(i), which lies in its place, is read.  Measured back to back, under the
+// power cap (32 / 8 heads of 128): 4096 tokens at 131072 in 8.2 ms, 1055 TFLOP/s (0.76
+// of the library product's sustained rate), 2048 at 65536 in 2.15 ms (1006); a prompt
+// of 8192 tokens 590 us (931), of 2048 75 us (458), where setting up (6 us), queries,
+// mask and epilogue of each item (some 5 us) and the joining of cut items (8 us)
+// count.  At D = 64 the MMAs take half, the exponentials the same: 690 TFLOP/s for
+// 4096 tokens at 16384, 510 for ragged chunks.
 //
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D) columns.
 // SMEM: Q0 Q1, K and V double buffered, 128 rows x D each, 128-byte swizzled in
@@ -59,8 +59,8 @@ constexpr int kMinTiles = 2;
 // What an item costs beside its tiles (2.1 us each): its queries' load, the
 // cleaning at the mask and the epilogue take some 5 us.  With no cost counted,
 // the workers of a short prompt's first items ended after 92 us and those of its
-// last after 50.  1, 2, 3, 4, 5 tiles: 79, 78, 75, 75, 75 us for 2048 tokens, 588,
-// 558, 544, 547, 553 for 8192.
+// last after 50.  1, 2, 3, 4, 5 tiles, one run: 79, 78, 75, 75, 75 us for 2048 tokens,
+// 588, 558, 544, 547, 553 for 8192 (590 back to back under the power cap).
 constexpr int kItemCost = 3;
 constexpr int kReaders = 11;             // warps 0-10 read the planner's parts
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 64;

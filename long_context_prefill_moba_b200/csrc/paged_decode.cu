@@ -15,8 +15,8 @@
 //     moved only when a row's max passes it by 2^8, probabilities rounded to bf16
 //     for the product (2^-9 of each, the sum l unrounded);
 //   - items cut by a worker's border are joined by the combine kernel.
-// Measured (32 / 8 heads of 128): 64 sequences of up to 16K keys, 2.6 GB, in 400 us
-// (6.5 TB/s, the copy benchmark's rate); 131072 keys of one sequence, 0.54 GB, in 86
+// Measured (32 / 8 heads of 128): 64 sequences of up to 16K keys, 2.6 GB, in 408 us
+// (6.4 TB/s, 0.98 of the copy benchmark's rate); 131072 keys of one sequence, 0.54 GB, in 86
 // us and 8 more for joining the 74 parts of each head; the smallest call 11 us,
 // some eight memory latencies one after another in the two kernels.
 // In tiles that some row does not see whole, slots behind the sequence's end and
