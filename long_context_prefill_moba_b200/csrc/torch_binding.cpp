@@ -6,6 +6,7 @@
 // times the kernels of a small step.  No arithmetic lives here.
 #include <ATen/cuda/CUDAContext.h>
 #include <c10/core/DeviceGuard.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/extension.h>
 
 #include "moba.h"
@@ -42,8 +43,10 @@ int32_t i32(int64_t v, const char* where) {
   REQUIRE(v >= 0 && v <= INT32_MAX, where, "a size beyond 32 bits");
   return (int32_t)v;
 }
-// a tangent (forward-mode AD) does not make a tensor require a gradient, and would be lost
+// a tangent (forward-mode AD) does not make a tensor require a gradient, and would be lost;
+// outside a dual level no tensor has one (asking each took 0.1 to 0.2 us of a call's 6)
 void no_tangents(std::initializer_list<const Tensor*> ts, const char* where) {
+  if (torch::autograd::ForwardADLevel::try_get_by_idx(0) == nullptr) return;
   for (const Tensor* t : ts)
     TORCH_CHECK(t == nullptr || !t->_fw_grad(/*level=*/0).defined(), where, ": has no forward-mode derivative");
 }
